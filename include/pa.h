@@ -71,6 +71,8 @@ typedef enum {
 #define PA_FLAG_BAD_PAIR 0x4    /* copy: src or dst outside [0, num_blocks) */
 #define PA_FLAG_BAD_LEN 0x8     /* decode: seq_len < 0, > max_seq_len, or > table capacity */
 #define PA_FLAG_TIMEOUT 0x10    /* a bounded in-kernel wait ran out */
+#define PA_FLAG_NO_BLOCKS 0x20  /* extend: the free list holds fewer blocks than the call needs */
+#define PA_FLAG_BAD_TREE 0x40   /* tree masks: a parent that is not an earlier node of its tree */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *pa_status_string(int status);
@@ -503,6 +505,223 @@ int pa_decode_append_fp8(float *out, const void *q, const void *k_new, const voi
                          int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
                          float k_scale, float v_scale, int partition_tokens, void *workspace,
                          size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Drafting and verifying several tokens in one step.
+ *
+ * The pages describe a step that appends one token to each sequence.  A
+ * program that drafts a tree of candidate tokens for each sequence, verifies
+ * all of them at once and keeps one path runs these calls, all on the device
+ * and capturable, around its model:
+ *
+ *     pa_tree_masks     parents of the drafted tokens -> ancestor masks, positions
+ *     pa_rope           rotary positions on the drafted tokens' q and k
+ *     pa_decode_tree    attention over the cache and the drafted ancestors
+ *     pa_extend_tables  blocks and slots for the accepted tokens (-1: rejected)
+ *     pa_reshape_and_cache   writes the accepted rows into the cache
+ *
+ * Drafted rows stay in the caller's own buffers until they are accepted, so a
+ * rejected token never takes room in a block.  Rows of all sequences are
+ * packed: sequence b owns rows [cu_nodes[b], cu_nodes[b+1]) of every
+ * row-indexed array, its nodes 0, 1, ...
+ * ---------------------------------------------------------------------- */
+
+/* Masks and positions of drafted trees.
+ *
+ * parents  : device int32 [num_rows]; parents[r] is the number, within its
+ *            sequence, of the node before node r - cu_nodes[b], or -1 for a
+ *            node that follows the last cached token.  A parent comes before
+ *            its children; one that does not (>= the node's own number, or
+ *            < -1) sets PA_FLAG_BAD_TREE and reads as -1.
+ * cu_nodes : device int32 [batch + 1], cu_nodes[0] <= ... <= cu_nodes[batch];
+ *            bounds that decrease or leave [0, num_rows] are cut and set
+ *            PA_FLAG_BAD_LEN.
+ * seq_lens : device int32 [batch], the tokens already cached
+ * max_nodes: at least every sequence's node count, at most
+ *            PA_TREE_MAX_NODES (else PA_ERR_UNSUPPORTED).  Nodes from
+ *            max_nodes on set PA_FLAG_BAD_LEN and get an empty mask.
+ * masks    : device int32 [num_rows, ceil(max_nodes / 32)]: bit j % 32 of word
+ *            j / 32 of row r is set when node j is r's node or an ancestor
+ *            of it
+ * positions: device int32 [num_rows] (may be NULL): seq_lens[b] + depth, 0
+ *            ancestors being depth 0
+ * Rows that belong to no sequence get an empty mask and position 0.
+ * batch == 0 or num_rows == 0 launches nothing. */
+#define PA_TREE_MAX_NODES 512
+
+int pa_tree_masks(int32_t *masks, int32_t *positions, const int32_t *parents, const int32_t *cu_nodes,
+                  const int32_t *seq_lens, int batch, int num_rows, int max_nodes, int32_t *err_flag,
+                  void *stream);
+
+/* Attention of drafted tokens over the paged cache and their own tree.
+ *
+ * For row r = cu_nodes[b] + i and query head g, with kv head
+ * h = g / (num_q_heads / num_kv_heads), over the cached tokens p < seq_lens[b]
+ * (addressed as in pa_decode) and the nodes j of the same sequence whose bit j
+ * is set in row r of `masks`:
+ *
+ *   out[r,g,:] = sum exp(scale q[r,g].k - max) v / sum exp(scale q[r,g].k - max)
+ *
+ * A row that sees nothing (no cached token, no bit) is zero; one whose scores
+ * are all -inf is NaN, as in pa_decode.  What a row does
+ * not see has no part in it, whatever it holds: infinities and NaN in the
+ * tail of a block, in a node that is not an ancestor or in the rows of
+ * another sequence stay out.
+ *
+ * out            : device bf16 [num_rows, num_q_heads, head_dim]; rows that
+ *                  belong to no sequence are left as they were
+ * q              : device bf16, row r at q + r * q_stride elements,
+ *                  [num_q_heads, head_dim] contiguous within the row
+ * k_tree, v_tree : device bf16 rows [num_kv_heads, head_dim] at strides
+ *                  k_stride, v_stride, rotated and ready to be cached.
+ *                  Strides are multiples of 8 elements and no smaller than
+ *                  a row; buffers are 16-byte aligned.
+ * seq_lens       : device int32 [batch], cached tokens, the drafted ones not
+ *                  counted
+ * cu_nodes       : as in pa_tree_masks.  Rows past max_nodes of a sequence
+ *                  set PA_FLAG_BAD_LEN and are left as they were.
+ * masks          : device int32 [num_rows, ceil(max_nodes / 32)], any bits
+ *                  (pa_tree_masks gives those of a tree); bits past the
+ *                  sequence's nodes are not looked at.  NULL: a chain, node i
+ *                  sees nodes 0..i.
+ * partition_tokens: 0 = library default, -1 = no split, > 0 = tokens of the
+ *                  cache for each partition, a multiple of 128
+ * workspace      : pa_decode_tree_workspace_size(...) bytes, 16-byte aligned
+ *                  (may be NULL if that is 0); no initialisation needed.
+ * A block id outside [0, num_blocks) sets PA_FLAG_BAD_BLOCK and its tokens
+ * are left out.  Other arguments, layouts and errors: as pa_decode.
+ * Products take bf16 operands and accumulate in fp32; the softmax is fp32. */
+size_t pa_decode_tree_workspace_size(int batch, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int block_size, int max_seq_len, int max_nodes, int partition_tokens);
+
+int pa_decode_tree_partition_tokens(int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int max_seq_len, int max_nodes, int partition_tokens);
+
+int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tree, int64_t k_stride,
+                   const void *v_tree, int64_t v_stride, int num_rows, const void *k_cache, const void *v_cache,
+                   const int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                   const int32_t *cu_nodes, const int32_t *masks, int batch, int max_seq_len, int max_nodes,
+                   int num_q_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                   float scale, int partition_tokens, void *workspace, size_t workspace_bytes,
+                   int32_t *err_flag, void *stream);
+
+/* Block tables grown on the device, with the slots and positions of the new
+ * tokens: what pa_alloc_step does on the host, for a program that keeps its
+ * lengths on the GPU.  Sequence b goes from seq_lens[b] to
+ * seq_lens[b] + add_lens[b] tokens; the blocks it needs beyond
+ * ceil(seq_lens[b] / block_size) are taken from the free list in order of b
+ * and written to its table ("Walk through paged attention end to end", append
+ * step: a new block when the position is a multiple of the block size).
+ * seq_lens all 0 builds the tables from the lengths alone.
+ *
+ * block_tables  : device int32 [batch, max_blocks_per_seq]; only the new
+ *                 entries are written.  A partly filled last block must
+ *                 belong to its sequence alone (as in pa_decode_append).
+ * seq_lens, add_lens : device int32 [batch].  A negative value, or a sum above
+ *                 max_blocks_per_seq * block_size, sets PA_FLAG_BAD_LEN and
+ *                 the sequence gets no token.
+ * seq_lens_out  : device int32 [batch], the new lengths; may be seq_lens
+ * free_blocks   : device int32 [num_free], block ids; entries from
+ *                 free_cursor[0] on are free.  An id outside [0, num_blocks)
+ *                 sets PA_FLAG_BAD_BLOCK and the slots in it are -1.
+ * free_cursor_out : device int32 [1], free_cursor plus the blocks taken; may be
+ *                 free_cursor
+ * slot_mapping  : device int32 [num_rows], for pa_reshape_and_cache
+ * positions     : device int32 [num_rows] (may be NULL), the position of each
+ *                 new token in its sequence, 0 where the slot is -1 because
+ *                 the row holds no new token
+ * cu_tokens     : device int32 [batch + 1], new tokens before each sequence
+ * cu_rows, path : both NULL: token i of sequence b is row cu_tokens[b] + i;
+ *                 rows past the last token get slot -1.
+ *                 Both given: rows are those of a drafted tree, sequence b's
+ *                 starting at cu_rows[b] (device int32 [batch + 1]), and its
+ *                 k-th new token is node path[b, k] (device int32
+ *                 [batch, max_path]; a node named twice counts where it is
+ *                 named first).  All other rows get slot -1.  add_lens[b] >
+ *                 max_path sets PA_FLAG_BAD_LEN, the sequence gets no token.
+ * All or nothing: when the free list does not hold the blocks
+ * (PA_FLAG_NO_BLOCKS), or num_rows does not hold the packed tokens
+ * (PA_FLAG_BAD_LEN), lengths, tables and cursor stay as they were, every slot
+ * is -1 and cu_tokens is all zero.
+ * No two pointers overlap except where it says so.  batch == 0 launches
+ * nothing. */
+int pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                     const int32_t *add_lens, int32_t *seq_lens_out, int batch, int block_size,
+                     int64_t num_blocks, const int32_t *free_blocks, int num_free, const int32_t *free_cursor,
+                     int32_t *free_cursor_out, int32_t *slot_mapping, int32_t *positions, int32_t *cu_tokens,
+                     int num_rows, const int32_t *cu_rows, const int32_t *path, int max_path,
+                     int32_t *err_flag, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.  With a_i = 2 pi * positions[t] * turns[i], pair i of the
+ * first rotary_dim values of every head becomes
+ *
+ *   (x, y) -> gain * (x cos a_i - y sin a_i, y cos a_i + x sin a_i)
+ *
+ * where pair i is (value i, value i + rotary_dim / 2), or, with
+ * interleaved != 0, (value 2i, value 2i + 1); the other values pass through.
+ * Angles are reduced in fp64, so positions far into a long context keep their
+ * phase; the rotation is fp32 and rounded once, to bf16 or to E4M3.
+ *
+ * q, k, v   : device bf16, row t at t * stride elements, heads contiguous
+ *             within the row ([heads, head_dim]): whole tensors or the parts
+ *             of one projection's output.  Strides are multiples of 8 and no
+ *             smaller than a row; buffers are 16-byte aligned.
+ * q_out, k_out : rows as q and k, with strides of their own; may be q and k
+ *             themselves (same stride), else no overlap with any input
+ * positions : device int32 [num_tokens]
+ * turns     : device double [rotary_dim / 2], from pa_rope_frequencies
+ * rotary_dim: a multiple of 16, 16 .. head_dim (else PA_ERR_UNSUPPORTED)
+ * num_q_heads 0 (q and q_out NULL) leaves q out.
+ *
+ * pa_rope writes the rotated k to k_out (num_kv_heads 0 leaves it out).
+ * pa_rope_and_cache writes the rotated k and v into the pools at
+ * slot_mapping, as pa_reshape_and_cache would (same rules for -1, for slots
+ * out of range and for slots named twice); pa_rope_and_cache_fp8 quantises
+ * them as pa_reshape_and_cache_fp8 does, straight from the fp32 rotation.
+ * One launch; num_tokens == 0 launches nothing.
+ * ---------------------------------------------------------------------- */
+int pa_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, int num_q_heads, const void *k,
+            int64_t k_stride, void *k_out, int64_t k_out_stride, int num_kv_heads, const int32_t *positions,
+            const double *turns, int rotary_dim, int interleaved, float gain, int num_tokens, int head_dim,
+            void *stream);
+
+int pa_rope_and_cache(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, int num_q_heads,
+                      const void *k, int64_t k_stride, const void *v, int64_t v_stride, int num_kv_heads,
+                      void *k_cache, void *v_cache, const int32_t *slot_mapping, int64_t num_blocks,
+                      int block_size, const int32_t *positions, const double *turns, int rotary_dim,
+                      int interleaved, float gain, int num_tokens, int head_dim, int32_t *err_flag, void *stream);
+
+int pa_rope_and_cache_fp8(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, int num_q_heads,
+                          const void *k, int64_t k_stride, const void *v, int64_t v_stride, int num_kv_heads,
+                          void *k_cache, void *v_cache, const int32_t *slot_mapping, int64_t num_blocks,
+                          int block_size, const int32_t *positions, const double *turns, int rotary_dim,
+                          int interleaved, float gain, int num_tokens, int head_dim, float k_scale,
+                          float v_scale, int32_t *err_flag, void *stream);
+
+/* Frequencies of the rotary pairs, in turns for each position, and the gain on
+ * the rotated values.  With f_i = base^(-2i / rotary_dim):
+ *   NONE       f_i
+ *   LINEAR     f_i / factor (positions interpolated)
+ *   NTK        the base becomes base * factor^(rotary_dim / (rotary_dim - 2))
+ *   BY_PARTS   pairs that turn more than `high` times within original_len keep
+ *              f_i, those that turn less than `low` times get f_i / factor, with
+ *              a linear ramp over the pair number between; gain 0.1 ln(factor) + 1
+ *              (the published YaRN method; low 1, high 32 are usual)
+ *   BY_WAVELENGTH  the same idea with the ramp over the number of turns
+ *              (low 1, high 4 are usual); gain 1
+ * turns: host double [rotary_dim / 2]; gain: host float [1]; host memory, no
+ * launch.  rotary_dim even and > 0 (NTK: > 2), base > 1, factor >= 1,
+ * original_len > 0 and 0 < low < high where they are used; else
+ * PA_ERR_INVALID_ARG, and an unknown scaling PA_ERR_UNSUPPORTED. */
+#define PA_ROPE_NONE 0
+#define PA_ROPE_LINEAR 1
+#define PA_ROPE_NTK 2
+#define PA_ROPE_BY_PARTS 3
+#define PA_ROPE_BY_WAVELENGTH 4
+
+int pa_rope_frequencies(double *turns, float *gain, int rotary_dim, double base, int scaling, double factor,
+                        double original_len, double low, double high);
 
 /* ------------------------------------------------------------------------
  * Host block allocator (owns host memory only; not thread-safe).

@@ -10,6 +10,11 @@ Device ops on bf16 pools (names as in the C ABI):
     pa_decode_append, pa_decode_shared_prefix, pa_decode_builtin_scratch,
     pa_decode_workspace_size, pa_decode_shared_prefix_workspace_size,
     pa_decode_partition_tokens
+Drafting and verifying several tokens in one step:
+    pa_tree_masks, pa_decode_tree, pa_decode_tree_workspace_size,
+    pa_decode_tree_partition_tokens, pa_extend_tables
+Rotary positions, alone or with the cache write:
+    pa_rope, pa_rope_and_cache, pa_rope_and_cache_fp8, pa_rope_frequencies
 Device ops on fp8 (E4M3) pools:
     pa_quantize_fp8, pa_reshape_and_cache_fp8, pa_copy_blocks_fp8,
     pa_swap_blocks_fp8, pa_decode_fp8 (with k_new/v_new: the fused write)
@@ -43,6 +48,10 @@ PA_FLAG_BAD_BLOCK = 0x2
 PA_FLAG_BAD_PAIR = 0x4
 PA_FLAG_BAD_LEN = 0x8
 PA_FLAG_TIMEOUT = 0x10
+PA_FLAG_NO_BLOCKS = 0x20
+PA_FLAG_BAD_TREE = 0x40
+
+PA_TREE_MAX_NODES = 512
 
 
 class PaError(RuntimeError):
@@ -361,6 +370,223 @@ class DecodeStepHost:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------------------
+# Drafting and verifying several tokens in one step
+# ---------------------------------------------------------------------------
+
+def _here(t, dtype, name):
+    """Pointer of a contiguous tensor on the current device (None passes as NULL)."""
+    if t is None:
+        return None
+    p = _dev(t, dtype, name)
+    if t.device.index != _torch().cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return p
+
+
+def _rows(t, heads, name):
+    """Pointer and row stride (elements) of bf16 rows [T, heads, d] whose heads are contiguous within a row."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    n, h, d = t.shape
+    if h != heads:
+        raise ValueError(f"{name} must hold {heads} heads, got {h}")
+    row, head, one = t.stride()
+    if t.numel() and ((one != 1 and d > 1) or (head != d and h > 1)):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (row if n > 1 else h * d)
+
+
+def pa_tree_masks(masks, positions, parents, cu_nodes, seq_lens, *, max_nodes: int, err_flag=None,
+                  stream=None) -> None:
+    """Ancestor masks (int32 [T, ceil(max_nodes/32)]) and positions (int32 [T], may be None) of drafted trees from
+    ``parents`` int32 [T] (-1: follows the cache), ``cu_nodes`` int32 [B+1] and the cached lengths int32 [B]."""
+    torch = _torch()
+    T, B, i32 = parents.numel(), seq_lens.numel(), torch.int32
+    if cu_nodes.numel() != B + 1 or tuple(masks.shape) != (T, -(-max_nodes // 32)):
+        raise ValueError("cu_nodes must be [B+1] and masks [T, ceil(max_nodes/32)]")
+    if positions is not None and positions.numel() != T:
+        raise ValueError("positions must have one entry per row")
+    _check(lib.pa_tree_masks(_here(masks, i32, "masks"), _here(positions, i32, "positions"),
+                             _here(parents, i32, "parents"), _here(cu_nodes, i32, "cu_nodes"),
+                             _here(seq_lens, i32, "seq_lens"), B, T, int(max_nodes), _opt_flag(err_flag),
+                             _stream(stream)), "pa_tree_masks")
+
+
+def pa_decode_tree_workspace_size(batch, num_rows, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
+                                  max_nodes, partition_tokens=0) -> int:
+    return int(lib.pa_decode_tree_workspace_size(batch, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                 max_seq_len, max_nodes, partition_tokens))
+
+
+def pa_decode_tree_partition_tokens(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, max_nodes,
+                                    partition_tokens=0) -> int:
+    return int(lib.pa_decode_tree_partition_tokens(batch, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                   max_seq_len, max_nodes, partition_tokens))
+
+
+def pa_decode_tree(out, q, k_tree, v_tree, k_cache, v_cache, block_tables, seq_lens, cu_nodes, masks, *,
+                   max_seq_len: int, max_nodes: int, scale: float, partition_tokens: int = 0, workspace=None,
+                   err_flag=None, stream=None) -> None:
+    """Attention of drafted rows: out bf16 [T, Hq, d] <- q [T, Hq, d] over the cached tokens of each sequence and the
+    drafted rows (k_tree, v_tree [T, Hkv, d]) its mask names (``masks`` int32 [T, ceil(max_nodes/32)]; None: a chain).
+
+    Rows of sequence b are [cu_nodes[b], cu_nodes[b+1]); q, k_tree and v_tree may be parts of one projection's output.
+    """
+    torch = _torch()
+    i32, bf16 = torch.int32, torch.bfloat16
+    T, Hq, d = q.shape
+    NB, Hkv, bs, d2 = k_cache.shape
+    B = seq_lens.numel()
+    if d2 != d or out.shape != q.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch")
+    if tuple(k_tree.shape) != (T, Hkv, d) or v_tree.shape != k_tree.shape:
+        raise ValueError("k_tree/v_tree must be [T, Hkv, d]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or cu_nodes.numel() != B + 1:
+        raise ValueError("block_tables must be [B, max_blocks], seq_lens [B] and cu_nodes [B+1]")
+    if masks is not None and tuple(masks.shape) != (T, -(-max_nodes // 32)):
+        raise ValueError("masks must be [T, ceil(max_nodes/32)]")
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr = _here(workspace, workspace.dtype, "workspace")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib.pa_decode_tree(
+        _here(out, bf16, "out"), *_rows(q, Hq, "q"), *_rows(k_tree, Hkv, "k_tree"), *_rows(v_tree, Hkv, "v_tree"), T,
+        _here(k_cache, bf16, "k_cache"), _here(v_cache, bf16, "v_cache"), _here(block_tables, i32, "block_tables"),
+        block_tables.shape[1], _here(seq_lens, i32, "seq_lens"), _here(cu_nodes, i32, "cu_nodes"),
+        _here(masks, i32, "masks"), B, int(max_seq_len), int(max_nodes), Hq, Hkv, d, bs, NB, float(scale),
+        int(partition_tokens), ws_ptr, ws_bytes, _opt_flag(err_flag), _stream(stream)), "pa_decode_tree")
+
+
+def pa_extend_tables(block_tables, seq_lens, add_lens, free_blocks, free_cursor, *, num_blocks: int, block_size: int,
+                     slot_mapping, cu_tokens, positions=None, seq_lens_out=None, cursor_out=None, cu_rows=None,
+                     path=None, err_flag=None, stream=None) -> None:
+    """Append ``add_lens`` tokens to each sequence on the device: new table entries from the free list, the slots and
+    positions of the new tokens, the new lengths and the list's new cursor.
+
+    ``seq_lens_out`` and ``cursor_out`` default to updating ``seq_lens`` and ``free_cursor`` in place.  With
+    ``cu_rows`` int32 [B+1] and ``path`` int32 [B, max_path] the slots go to the accepted rows of drafted trees.
+    """
+    i32 = _torch().int32
+    B, T = seq_lens.numel(), slot_mapping.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or add_lens.numel() != B or cu_tokens.numel() != B + 1:
+        raise ValueError("block_tables must be [B, max_blocks], add_lens [B] and cu_tokens [B+1]")
+    if positions is not None and positions.numel() != T:
+        raise ValueError("positions must have one entry per row")
+    if (cu_rows is None) != (path is None):
+        raise ValueError("pass both cu_rows and path, or neither")
+    if path is not None and (path.dim() != 2 or path.shape[0] != B or cu_rows.numel() != B + 1):
+        raise ValueError("cu_rows must be [B+1] and path [B, max_path]")
+    lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    cur_out = free_cursor if cursor_out is None else cursor_out
+    if lens_out.numel() != B or free_cursor.numel() != 1 or cur_out.numel() != 1:
+        raise ValueError("seq_lens_out must be [B], the cursors one entry")
+    _check(lib.pa_extend_tables(
+        _here(block_tables, i32, "block_tables"), block_tables.shape[1], _here(seq_lens, i32, "seq_lens"),
+        _here(add_lens, i32, "add_lens"), _here(lens_out, i32, "seq_lens_out"), B, int(block_size), int(num_blocks),
+        _here(free_blocks, i32, "free_blocks"), free_blocks.numel(), _here(free_cursor, i32, "free_cursor"),
+        _here(cur_out, i32, "cursor_out"), _here(slot_mapping, i32, "slot_mapping"),
+        _here(positions, i32, "positions"), _here(cu_tokens, i32, "cu_tokens"), T, _here(cu_rows, i32, "cu_rows"),
+        _here(path, i32, "path"), 0 if path is None else path.shape[1], _opt_flag(err_flag), _stream(stream)),
+        "pa_extend_tables")
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3, "by_wavelength": 4}
+
+
+def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                        original_len: float = 8192.0, low: Optional[float] = None, high: Optional[float] = None):
+    """Frequencies of the rotary pairs as a double CPU tensor [rotary_dim/2] (turns for each position; move it to the
+    device once) and the gain on the rotated values."""
+    torch = _torch()
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    if low is None:
+        low = 1.0
+    if high is None:
+        high = 4.0 if scaling == "by_wavelength" else 32.0
+    turns = torch.empty(max(rotary_dim // 2, 0), dtype=torch.float64)
+    gain = ctypes.c_float()
+    _check(lib.pa_rope_frequencies(ctypes.c_void_p(turns.data_ptr()), ctypes.byref(gain), int(rotary_dim), float(base),
+                                   ROPE_SCALINGS[scaling], float(factor), float(original_len), float(low),
+                                   float(high)), "pa_rope_frequencies")
+    return turns, gain.value
+
+
+def _rope_args(q, q_out, positions, turns, T, d):
+    torch = _torch()
+    if (q is None) != (q_out is None):
+        raise ValueError("pass both q and q_out, or neither")
+    if positions.numel() != T:
+        raise ValueError("positions must have one entry per token")
+    head = (None, 0, None, 0, 0)
+    if q is not None:
+        Hq = q.shape[1]
+        if q.shape != q_out.shape or q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q and q_out must be [T, Hq, d]")
+        head = (*_rows(q, Hq, "q"), *_rows(q_out, Hq, "q_out"), Hq)
+    tail = (_here(positions, torch.int32, "positions"), _here(turns, torch.float64, "turns"), 2 * turns.numel())
+    return head, tail
+
+
+def pa_rope(q, q_out, k, k_out, positions, turns, *, interleaved: bool = False, gain: float = 1.0,
+            stream=None) -> None:
+    """Rotate q [T, Hq, d] into q_out and k [T, Hkv, d] into k_out (each pair may be None, or one tensor twice)."""
+    if (k is None) != (k_out is None):
+        raise ValueError("pass both k and k_out, or neither")
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("nothing to rotate")
+    T, _, d = some.shape
+    head, tail = _rope_args(q, q_out, positions, turns, T, d)
+    keys = (None, 0, None, 0, 0)
+    if k is not None:
+        if k.shape != k_out.shape or k.shape[0] != T or k.shape[2] != d:
+            raise ValueError("k and k_out must be [T, Hkv, d]")
+        keys = (*_rows(k, k.shape[1], "k"), *_rows(k_out, k.shape[1], "k_out"), k.shape[1])
+    _check(lib.pa_rope(*head, *keys, *tail, int(bool(interleaved)), float(gain), T, d, _stream(stream)), "pa_rope")
+
+
+def _rope_and_cache(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, pool_dtype):
+    T, Hkv, d = k.shape
+    NB, Hkv2, bs, d2 = k_cache.shape
+    if (Hkv2, d2) != (Hkv, d) or v.shape != k.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch")
+    if slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must have one entry per token")
+    head, tail = _rope_args(q, q_out, positions, turns, T, d)
+    return (*head, *_rows(k, Hkv, "k"), *_rows(v, Hkv, "v"), Hkv, _here(k_cache, pool_dtype, "k_cache"),
+            _here(v_cache, pool_dtype, "v_cache"), _here(slot_mapping, _torch().int32, "slot_mapping"), NB, bs, *tail)
+
+
+def pa_rope_and_cache(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, *, interleaved: bool = False,
+                      gain: float = 1.0, err_flag=None, stream=None) -> None:
+    """Rotate q [T, Hq, d] into q_out (both may be None) and write the rotated k and v [T, Hkv, d] into the bf16 pools
+    at slot_mapping [T], in one launch."""
+    args = _rope_and_cache(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, _torch().bfloat16)
+    _check(lib.pa_rope_and_cache(*args, int(bool(interleaved)), float(gain), k.shape[0], k.shape[2],
+                                 _opt_flag(err_flag), _stream(stream)), "pa_rope_and_cache")
+
+
+def pa_rope_and_cache_fp8(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, *, k_scale: float,
+                          v_scale: float, interleaved: bool = False, gain: float = 1.0, err_flag=None,
+                          stream=None) -> None:
+    """pa_rope_and_cache over uint8 E4M3 pools: the rotated k and v are quantised as they are written."""
+    args = _rope_and_cache(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, _torch().uint8)
+    _check(lib.pa_rope_and_cache_fp8(*args, int(bool(interleaved)), float(gain), k.shape[0], k.shape[2],
+                                     float(k_scale), float(v_scale), _opt_flag(err_flag), _stream(stream)),
+           "pa_rope_and_cache_fp8")
 
 
 # ---------------------------------------------------------------------------

@@ -17,6 +17,7 @@ _I64 = ctypes.c_int64
 _U64 = ctypes.c_uint64
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_D = ctypes.c_double
 _PI = ctypes.POINTER(ctypes.c_int)
 
 # name -> (restype, argtypes); mirrors include/pa.h
@@ -54,6 +55,18 @@ SIGNATURES = {
                            _P]),
     "pa_decode_append_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I64, _F, _F, _F, _I,
                                   _P, _SZ, _P, _P]),
+    "pa_tree_masks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "pa_decode_tree_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "pa_decode_tree_partition_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "pa_decode_tree": (_I, [_P, _P, _I64, _P, _I64, _P, _I64, _I, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                            _I, _I64, _F, _I, _P, _SZ, _P, _P]),
+    "pa_extend_tables": (_I, [_P, _I, _P, _P, _P, _I, _I, _I64, _P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P, _P]),
+    "pa_rope": (_I, [_P, _I64, _P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _P, _I, _I, _F, _I, _I, _P]),
+    "pa_rope_and_cache": (_I, [_P, _I64, _P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _P, _P, _I64, _I, _P, _P, _I, _I,
+                               _F, _I, _I, _P, _P]),
+    "pa_rope_and_cache_fp8": (_I, [_P, _I64, _P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _P, _P, _I64, _I, _P, _P, _I,
+                                   _I, _F, _I, _I, _F, _F, _P, _P]),
+    "pa_rope_frequencies": (_I, [_P, _P, _I, _D, _I, _D, _D, _D, _D]),
     "pa_alloc_create": (_I, [_I, _I, ctypes.POINTER(_P)]),
     "pa_alloc_create_ordered": (_I, [_I, _I, _P, ctypes.POINTER(_P)]),
     "pa_alloc_destroy": (None, [_P]),
