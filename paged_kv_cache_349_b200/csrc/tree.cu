@@ -1,98 +1,137 @@
-// Attention of drafted tokens over the paged cache and over their own tree.
-//
-// Row r (node i of sequence b) and query head g:
-//   out = sum_j exp(scale q.k_j - m) v_j / sum_j exp(scale q.k_j - m)
-// over the sequence's cached tokens and the nodes its mask names.
-//
-// One warp computes one (row, query head): the lanes share the head dimension,
-// a running maximum and sum carry the softmax over the tokens.
-#include "pa_common.cuh"
+// Host side of the attention of drafted tokens: tensor maps, the split over the
+// cache's length, the workspace and the launches (the device code is in
+// tree_kernels.cuh).
+#include <mutex>
+
+#include "tree_kernels.cuh"
 
 namespace pa {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kTreeWarps = 8;
+using EncodeTiledFn = decltype(&cuTensorMapEncodeTiled);
 
-struct TreeParams {
-    uint16_t *out;
-    const uint16_t *q, *k_tree, *v_tree, *k_pool, *v_pool;
-    const int32_t *tables, *lens, *cu, *masks;
-    int32_t *err_flag;
-    int64_t q_stride, k_stride, v_stride, num_blocks;
-    int num_rows, batch, max_blocks, max_seq_len, max_nodes, words;
-    int q_heads, kv_heads, group, block_size;
-    float scale_log2;
+EncodeTiledFn tree_encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
+// bf16 tensor of `rank` dimensions, innermost first, read in boxes of 64 values
+// with the 128-byte swizzle; strides in bytes from the second dimension on.
+bool tree_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+              const cuuint32_t *box) {
+    EncodeTiledFn enc = tree_encode_fn();
+    if (!enc) return false;
+    const cuuint32_t step[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows [num_rows, heads, head_dim] at a row stride, read as `box_rows` rows of `box_heads` heads.
+bool tree_rows_map(CUtensorMap *map, const void *base, int64_t stride, int num_rows, int heads, int head_dim,
+                   int box_heads, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)num_rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    return tree_map(map, base, 3, dims, strides, box);
+}
+
+bool tree_pool_map(CUtensorMap *map, const void *base, uint64_t rows, int head_dim, int block_size) {
+    const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)head_dim * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)block_size};
+    return tree_map(map, base, 2, dims, strides, box);
+}
+
+// More than 128 query rows of a kv head: two streams of 128 rows share each K and V tile.
+int tree_streams(int max_nodes, int group) { return (int64_t)max_nodes * group > kTileM ? 2 : 1; }
+
+int tree_chunks(int max_nodes, int group) {
+    const int nodes = tree_streams(max_nodes, group) * (kTileM / group);
+    return (max_nodes + nodes - 1) / nodes;
+}
+
+// Tokens of one partition, -1 for no split.  The default weighs whole waves of
+// CTAs: each costs its share of the cache plus kFixed tokens' worth of start and end.
+int tree_partition(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, int max_nodes, int requested) {
+    if (requested < 0) return -1;
+    if (requested > 0) return requested >= max_seq_len ? -1 : requested;
+    const int group = num_q_heads / num_kv_heads;
+    const int64_t units = (int64_t)batch * num_kv_heads * tree_chunks(max_nodes, group);
+    const int64_t resident = (int64_t)device_sm_count() * (tree_streams(max_nodes, group) == 1 ? 2 : 1);
+    constexpr int64_t kFixed = 256;
+    int best = -1;
+    int64_t best_cost = 0;
+    for (int parts = 1; parts <= 64; ++parts) {
+        const int64_t tokens = ((max_seq_len + parts - 1) / parts + 127) / 128 * 128;
+        if (parts > 1 && tokens < 256) break;
+        const int64_t cost = (units * parts + resident - 1) / resident * (tokens + kFixed);
+        if (best < 0 || cost < best_cost) {
+            best = (int)tokens;
+            best_cost = cost;
+        }
+    }
+    return best >= max_seq_len ? -1 : best;
+}
+
+struct TreeLayout {
+    size_t ml, total;
 };
 
-template <int HEAD_DIM>
-__global__ void __launch_bounds__(kTreeWarps * 32) tree_kernel(const TreeParams p) {
-    constexpr int V = HEAD_DIM / 32;  // values of one lane
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.z, g = blockIdx.y, h = g / p.group;
-    const int i = blockIdx.x * kTreeWarps + (threadIdx.x >> 5);
-    const int lo = min(max(__ldg(p.cu + b), 0), p.num_rows);
-    const int hi = max(min(max(__ldg(p.cu + b + 1), 0), p.num_rows), lo);
-    const int nodes = min(hi - lo, p.max_nodes);
-    const int raw = __ldg(p.lens + b);
-    const int L = min(max(raw, 0), min(p.max_seq_len, p.max_blocks * p.block_size));
-    if (g == 0 && blockIdx.x == 0 && threadIdx.x == 0 &&
-        (raw != L || lo != __ldg(p.cu + b) || hi != __ldg(p.cu + b + 1) || nodes != hi - lo))
-        raise_flag(p.err_flag, PA_FLAG_BAD_LEN);
-    if (i >= nodes) return;
-    const int64_t r = lo + i;
+TreeLayout tree_layout(int num_rows, int num_q_heads, int head_dim, int64_t parts) {
+    const int64_t rows = (int64_t)num_rows * num_q_heads * parts;
+    TreeLayout l{};
+    l.ml = (size_t)((rows * head_dim * 4 + 255) / 256 * 256);
+    l.total = l.ml + (size_t)(rows * 2 * 4);
+    return l;
+}
 
-    auto load = [&](const uint16_t *src, float (&x)[V]) {
-#pragma unroll
-        for (int e = 0; e < V; e += 2) {
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(src + lane * V + e));
-            x[e] = bf16_lo_to_float(w);
-            x[e + 1] = bf16_hi_to_float(w);
+struct TreeMaps {
+    CUtensorMap q, k, v, kt, vt;
+};
+
+template <int HEAD_DIM, int STREAMS>
+int launch_tree(const TreeMaps &m, const TreeParams &p, cudaStream_t stream) {
+    using C = TreeCfg<HEAD_DIM, STREAMS>;
+    auto kern = tree_kernel<HEAD_DIM, STREAMS>;
+    {
+        // The shared-memory opt-in belongs to the kernel as loaded on one device: once per device.
+        static std::mutex mu;
+        static bool done[64] = {};
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done[dev]) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+                return PA_ERR_CUDA;
+            done[dev] = true;
         }
-    };
-    float q[V], o[V], m = -INFINITY, l = 0.f;
-    bool any = false;  // the row sees something
-    load(p.q + r * p.q_stride + g * HEAD_DIM, q);
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
-    auto take = [&](const uint16_t *k_row, const uint16_t *v_row) {
-        float k[V], v[V], s = 0.f;
-        load(k_row, k);
-        load(v_row, v);
-#pragma unroll
-        for (int e = 0; e < V; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= p.scale_log2;
-        any = true;
-        const float top = fmaxf(m, s);
-        const float ref = top == -INFINITY ? 0.f : top;  // nothing seen yet: weights 0, a NaN score stays NaN
-        const float down = exp2f(m - ref), w = exp2f(s - ref);
-        m = top;
-        l = l * down + w;
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = o[e] * down + w * v[e];
-    };
-    for (int t = 0; t < L; ++t) {
-        const int64_t phys = __ldg(p.tables + (int64_t)b * p.max_blocks + t / p.block_size);
-        if (phys < 0 || phys >= p.num_blocks) {
-            if (lane == 0) raise_flag(p.err_flag, PA_FLAG_BAD_BLOCK);
-            continue;
-        }
-        const int64_t row = ((phys * p.kv_heads + h) * p.block_size + t % p.block_size) * HEAD_DIM;
-        take(p.k_pool + row, p.v_pool + row);
     }
-    for (int j = 0; j < nodes; ++j) {
-        const bool seen = p.masks ? (__ldg(p.masks + r * p.words + (j >> 5)) >> (j & 31)) & 1 : j <= i;
-        if (seen)
-            take(p.k_tree + (int64_t)(lo + j) * p.k_stride + h * HEAD_DIM,
-                 p.v_tree + (int64_t)(lo + j) * p.v_stride + h * HEAD_DIM);
-    }
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (r * p.q_heads + g) * HEAD_DIM + lane * V);
-#pragma unroll
-    for (int e = 0; e < V; e += 2)
-        // nothing seen: zeros; all scores -inf: 0 / 0
-        dst[e / 2] = !any ? 0u : pack_bf16x2(o[e] / l, o[e + 1] / l);
+    const dim3 grid((unsigned)(p.chunks * p.num_parts), (unsigned)p.kv_heads, (unsigned)p.batch);
+    kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(m.q, m.k, m.v, m.kt, m.vt, p);
+    count_launch();
+    const int st = launch_status();
+    if (st != PA_OK || p.num_parts == 1) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.max_nodes * p.q_heads + kTreeReduceWarps - 1) / kTreeReduceWarps), (unsigned)p.batch);
+    cfg.blockDim = dim3(kTreeReduceWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_reduce_kernel<HEAD_DIM>, p);
+    count_launch();
+    return e == cudaSuccess ? launch_status() : PA_ERR_CUDA;
 }
 
 bool bad_rows(const void *p, int64_t stride, int heads, int head_dim) {
@@ -106,16 +145,18 @@ extern "C" {
 
 int pa_decode_tree_partition_tokens(int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                                     int max_seq_len, int max_nodes, int partition_tokens) {
-    (void)batch, (void)num_q_heads, (void)num_kv_heads, (void)head_dim, (void)block_size, (void)max_seq_len;
-    (void)max_nodes, (void)partition_tokens;
-    return -1;
+    if (batch <= 0 || max_seq_len <= 0 || max_nodes <= 0 ||
+        !pa::supported_shape(num_q_heads, num_kv_heads, head_dim, block_size))
+        return -1;
+    return pa::tree_partition(batch, num_q_heads, num_kv_heads, max_seq_len, max_nodes, partition_tokens);
 }
 
 size_t pa_decode_tree_workspace_size(int batch, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
                                      int block_size, int max_seq_len, int max_nodes, int partition_tokens) {
-    (void)batch, (void)num_rows, (void)num_q_heads, (void)num_kv_heads, (void)head_dim, (void)block_size;
-    (void)max_seq_len, (void)max_nodes, (void)partition_tokens;
-    return 0;
+    const int pt = pa_decode_tree_partition_tokens(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
+                                                   max_nodes, partition_tokens);
+    if (pt <= 0 || num_rows <= 0) return 0;
+    return pa::tree_layout(num_rows, num_q_heads, head_dim, ((int64_t)max_seq_len + pt - 1) / pt).total;
 }
 
 int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tree, int64_t k_stride,
@@ -125,7 +166,6 @@ int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tre
                    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
                    float scale, int partition_tokens, void *workspace, size_t workspace_bytes,
                    int32_t *err_flag, void *stream) {
-    (void)workspace, (void)workspace_bytes;
     if (batch < 0 || max_seq_len < 0 || max_nodes < 0 || num_rows < 0 || num_blocks <= 0 || max_blocks_per_seq < 0)
         return PA_ERR_INVALID_ARG;
     if (!pa::supported_shape(num_q_heads, num_kv_heads, head_dim, block_size)) return PA_ERR_UNSUPPORTED;
@@ -142,39 +182,50 @@ int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tre
     if (rows >= (1ull << 31)) return PA_ERR_UNSUPPORTED;  // TMA row coordinate is int32
     pa::TreeParams p{};
     p.out = static_cast<uint16_t *>(out);
-    p.q = static_cast<const uint16_t *>(q);
-    p.k_tree = static_cast<const uint16_t *>(k_tree);
     p.v_tree = static_cast<const uint16_t *>(v_tree);
-    p.k_pool = static_cast<const uint16_t *>(k_cache);
-    p.v_pool = static_cast<const uint16_t *>(v_cache);
     p.tables = block_tables;
     p.lens = seq_lens;
     p.cu = cu_nodes;
     p.masks = masks;
     p.err_flag = err_flag;
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
     p.v_stride = v_stride;
     p.num_blocks = num_blocks;
     p.num_rows = num_rows;
-    p.batch = batch;
     p.max_blocks = max_blocks_per_seq;
     p.max_seq_len = max_seq_len;
     p.max_nodes = max_nodes;
     p.words = (max_nodes + 31) / 32;
+    p.batch = batch;
     p.q_heads = num_q_heads;
     p.kv_heads = num_kv_heads;
     p.group = num_q_heads / num_kv_heads;
     p.block_size = block_size;
-    p.scale_log2 = scale * pa::kLog2e;
-    const dim3 grid((unsigned)((max_nodes + pa::kTreeWarps - 1) / pa::kTreeWarps), (unsigned)num_q_heads, (unsigned)batch);
+    p.pool_rows = (int)rows;
+    p.scale_log2 = scale * pa::kTreeLog2e;
+    p.chunks = pa::tree_chunks(max_nodes, p.group);
+    const int pt = max_seq_len > 0 ? pa::tree_partition(batch, num_q_heads, num_kv_heads, max_seq_len, max_nodes,
+                                                        partition_tokens)
+                                   : -1;
+    p.part_tokens = pt > 0 ? pt : (max_seq_len > 0 ? max_seq_len : 1);
+    p.num_parts = pt > 0 ? (max_seq_len + pt - 1) / pt : 1;
+    if (pt > 0) {
+        const pa::TreeLayout l = pa::tree_layout(num_rows, num_q_heads, head_dim, p.num_parts);
+        if (!workspace || workspace_bytes < l.total || !pa::aligned16(workspace)) return PA_ERR_INVALID_ARG;
+        p.part_o = static_cast<float *>(workspace);
+        p.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + l.ml);
+    }
+    if ((int64_t)p.chunks * p.num_parts > INT32_MAX || (int64_t)max_nodes * num_q_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    pa::TreeMaps m;
+    if (!pa::tree_rows_map(&m.q, q, q_stride, num_rows, num_q_heads, head_dim, p.group, pa::kTileM / p.group) ||
+        !pa::tree_rows_map(&m.kt, k_tree, k_stride, num_rows, num_kv_heads, head_dim, 1, pa::kTileN) ||
+        !pa::tree_rows_map(&m.vt, v_tree, v_stride, num_rows, num_kv_heads, head_dim, 1, pa::kTileN) ||
+        !pa::tree_pool_map(&m.k, k_cache, rows, head_dim, block_size) ||
+        !pa::tree_pool_map(&m.v, v_cache, rows, head_dim, block_size))
+        return PA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (head_dim == 128)
-        pa::tree_kernel<128><<<grid, pa::kTreeWarps * 32, 0, s>>>(p);
-    else
-        pa::tree_kernel<64><<<grid, pa::kTreeWarps * 32, 0, s>>>(p);
-    pa::count_launch();
-    return pa::launch_status();
+    if (pa::tree_streams(max_nodes, p.group) == 2)
+        return head_dim == 128 ? pa::launch_tree<128, 2>(m, p, s) : pa::launch_tree<64, 2>(m, p, s);
+    return head_dim == 128 ? pa::launch_tree<128, 1>(m, p, s) : pa::launch_tree<64, 1>(m, p, s);
 }
 
 }  // extern "C"
