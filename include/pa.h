@@ -584,8 +584,15 @@ int pa_tree_masks(int32_t *masks, int32_t *positions, const int32_t *parents, co
  *                  (pa_tree_masks gives those of a tree); bits past the
  *                  sequence's nodes are not looked at.  NULL: a chain, node i
  *                  sees nodes 0..i.
- * partition_tokens: 0 = library default, -1 = no split, > 0 = tokens of the
- *                  cache for each partition, a multiple of 128
+ * partition_tokens: the attention runs as one grid that fills the GPU and
+ *                  shares out all sequences' tiles evenly, which cuts some
+ *                  (sequence, kv head) pairs into pieces; a second kernel,
+ *                  launched as a programmatic dependent, joins them
+ *                  (log-sum-exp).  0 = library default (no cut when
+ *                  max_seq_len is at most 512 tokens), > 0 = a piece has about
+ *                  this many tokens or more (a multiple of 128; no cut when
+ *                  max_seq_len is at most twice that), -1 = no cut: results
+ *                  then do not depend on the rest of the batch.
  * workspace      : pa_decode_tree_workspace_size(...) bytes, 16-byte aligned
  *                  (may be NULL if that is 0); no initialisation needed.
  * A block id outside [0, num_blocks) sets PA_FLAG_BAD_BLOCK and its tokens
@@ -593,9 +600,6 @@ int pa_tree_masks(int32_t *masks, int32_t *positions, const int32_t *parents, co
  * Products take bf16 operands and accumulate in fp32; the softmax is fp32. */
 size_t pa_decode_tree_workspace_size(int batch, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
                                      int block_size, int max_seq_len, int max_nodes, int partition_tokens);
-
-int pa_decode_tree_partition_tokens(int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
-                                    int max_seq_len, int max_nodes, int partition_tokens);
 
 int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tree, int64_t k_stride,
                    const void *v_tree, int64_t v_stride, int num_rows, const void *k_cache, const void *v_cache,

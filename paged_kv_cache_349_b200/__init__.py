@@ -12,7 +12,7 @@ Device ops on bf16 pools (names as in the C ABI):
     pa_decode_partition_tokens
 Drafting and verifying several tokens in one step:
     pa_tree_masks, pa_decode_tree, pa_decode_tree_workspace_size,
-    pa_decode_tree_partition_tokens, pa_extend_tables
+    pa_extend_tables
 Rotary positions, alone or with the cache write:
     pa_rope, pa_rope_and_cache, pa_rope_and_cache_fp8, pa_rope_frequencies
 Device ops on fp8 (E4M3) pools:
@@ -424,12 +424,6 @@ def pa_decode_tree_workspace_size(batch, num_rows, num_q_heads, num_kv_heads, he
                                   max_nodes, partition_tokens=0) -> int:
     return int(lib.pa_decode_tree_workspace_size(batch, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
                                                  max_seq_len, max_nodes, partition_tokens))
-
-
-def pa_decode_tree_partition_tokens(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, max_nodes,
-                                    partition_tokens=0) -> int:
-    return int(lib.pa_decode_tree_partition_tokens(batch, num_q_heads, num_kv_heads, head_dim, block_size,
-                                                   max_seq_len, max_nodes, partition_tokens))
 
 
 def pa_decode_tree(out, q, k_tree, v_tree, k_cache, v_cache, block_tables, seq_lens, cu_nodes, masks, *,

@@ -57,7 +57,6 @@ SIGNATURES = {
                                   _P, _SZ, _P, _P]),
     "pa_tree_masks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
     "pa_decode_tree_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
-    "pa_decode_tree_partition_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "pa_decode_tree": (_I, [_P, _P, _I64, _P, _I64, _P, _I64, _I, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                             _I, _I64, _F, _I, _P, _SZ, _P, _P]),
     "pa_extend_tables": (_I, [_P, _I, _P, _P, _P, _I, _I, _I64, _P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P, _P]),

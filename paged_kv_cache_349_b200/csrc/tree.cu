@@ -1,5 +1,5 @@
-// Host side of the attention of drafted tokens: tensor maps, the split over the
-// cache's length, the workspace and the launches (the device code is in
+// Host side of the attention of drafted tokens: tensor maps, the choice of
+// variant, the workspace and the launches (the device code is in
 // tree_kernels.cuh).
 #include <mutex>
 
@@ -54,43 +54,33 @@ bool tree_pool_map(CUtensorMap *map, const void *base, uint64_t rows, int head_d
 // More than 128 query rows of a kv head: two streams of 128 rows share each K and V tile.
 int tree_streams(int max_nodes, int group) { return (int64_t)max_nodes * group > kTileM ? 2 : 1; }
 
-int tree_chunks(int max_nodes, int group) {
-    const int nodes = tree_streams(max_nodes, group) * (kTileM / group);
-    return (max_nodes + nodes - 1) / nodes;
+int tree_tile(int max_nodes, int group) { return tree_streams(max_nodes, group) == 2 ? TreeCfg<128, 2>::kTileN : TreeCfg<128, 1>::kTileN; }
+
+// CTAs that the device holds at once: the grid, whatever the batch.
+int tree_ctas(int max_nodes, int group) {
+    return device_sm_count() *
+           (tree_streams(max_nodes, group) == 2 ? TreeCfg<128, 2>::kCtasPerSm : TreeCfg<128, 1>::kCtasPerSm);
 }
 
-// Tokens of one partition, -1 for no split.  The default weighs whole waves of
-// CTAs: each costs its share of the cache plus kFixed tokens' worth of start and end.
-int tree_partition(int batch, int num_q_heads, int num_kv_heads, int max_seq_len, int max_nodes, int requested) {
+// Tokens that a piece of a cut unit has at least, or -1 when no unit is cut.  Caches that fit a few tiles
+// are left whole by default: the second launch would cost more than the balance gains.
+constexpr int kTreeShare = 256;
+int tree_share(int max_seq_len, int requested) {
     if (requested < 0) return -1;
-    if (requested > 0) return requested >= max_seq_len ? -1 : requested;
-    const int group = num_q_heads / num_kv_heads;
-    const int64_t units = (int64_t)batch * num_kv_heads * tree_chunks(max_nodes, group);
-    const int64_t resident = (int64_t)device_sm_count() * (tree_streams(max_nodes, group) == 1 ? 2 : 1);
-    constexpr int64_t kFixed = 256;
-    int best = -1;
-    int64_t best_cost = 0;
-    for (int parts = 1; parts <= 64; ++parts) {
-        const int64_t tokens = ((max_seq_len + parts - 1) / parts + 127) / 128 * 128;
-        if (parts > 1 && tokens < 256) break;
-        const int64_t cost = (units * parts + resident - 1) / resident * (tokens + kFixed);
-        if (best < 0 || cost < best_cost) {
-            best = (int)tokens;
-            best_cost = cost;
-        }
-    }
-    return best >= max_seq_len ? -1 : best;
+    const int share = requested > 0 ? requested : kTreeShare;
+    return max_seq_len <= 2 * share ? -1 : share;
 }
 
+// Workspace: two states for each CTA, of a unit that began before it and of one that ends after it.
 struct TreeLayout {
     size_t ml, total;
 };
 
-TreeLayout tree_layout(int num_rows, int num_q_heads, int head_dim, int64_t parts) {
-    const int64_t rows = (int64_t)num_rows * num_q_heads * parts;
+TreeLayout tree_layout(int ctas, int streams, int head_dim) {
+    const size_t rows = (size_t)ctas * 2 * streams * kTileM;
     TreeLayout l{};
-    l.ml = (size_t)((rows * head_dim * 4 + 255) / 256 * 256);
-    l.total = l.ml + (size_t)(rows * 2 * 4);
+    l.ml = rows * head_dim * 4;
+    l.total = l.ml + rows * 8;
     return l;
 }
 
@@ -115,21 +105,21 @@ int launch_tree(const TreeMaps &m, const TreeParams &p, cudaStream_t stream) {
             done[dev] = true;
         }
     }
-    const dim3 grid((unsigned)(p.chunks * p.num_parts), (unsigned)p.kv_heads, (unsigned)p.batch);
-    kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(m.q, m.k, m.v, m.kt, m.vt, p);
+    const int ctas = tree_ctas(p.max_nodes, p.group);
+    kern<<<ctas, C::kThreads, C::kSmemBytes, stream>>>(m.q, m.k, m.v, m.kt, m.vt, p);
     count_launch();
     const int st = launch_status();
-    if (st != PA_OK || p.num_parts == 1) return st;
+    if (st != PA_OK || !p.part_o) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.max_nodes * p.q_heads + kTreeReduceWarps - 1) / kTreeReduceWarps), (unsigned)p.batch);
-    cfg.blockDim = dim3(kTreeReduceWarps * 32);
+    cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)(STREAMS * kTileM / kJoinRows));
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_reduce_kernel<HEAD_DIM>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel<HEAD_DIM, STREAMS>, p);
     count_launch();
     return e == cudaSuccess ? launch_status() : PA_ERR_CUDA;
 }
@@ -143,20 +133,14 @@ bool bad_rows(const void *p, int64_t stride, int heads, int head_dim) {
 
 extern "C" {
 
-int pa_decode_tree_partition_tokens(int batch, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
-                                    int max_seq_len, int max_nodes, int partition_tokens) {
-    if (batch <= 0 || max_seq_len <= 0 || max_nodes <= 0 ||
-        !pa::supported_shape(num_q_heads, num_kv_heads, head_dim, block_size))
-        return -1;
-    return pa::tree_partition(batch, num_q_heads, num_kv_heads, max_seq_len, max_nodes, partition_tokens);
-}
-
 size_t pa_decode_tree_workspace_size(int batch, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
                                      int block_size, int max_seq_len, int max_nodes, int partition_tokens) {
-    const int pt = pa_decode_tree_partition_tokens(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
-                                                   max_nodes, partition_tokens);
-    if (pt <= 0 || num_rows <= 0) return 0;
-    return pa::tree_layout(num_rows, num_q_heads, head_dim, ((int64_t)max_seq_len + pt - 1) / pt).total;
+    if (batch <= 0 || num_rows <= 0 || max_seq_len <= 0 || max_nodes <= 0 ||
+        !pa::supported_shape(num_q_heads, num_kv_heads, head_dim, block_size) ||
+        pa::tree_share(max_seq_len, partition_tokens) < 0)
+        return 0;
+    const int group = num_q_heads / num_kv_heads;
+    return pa::tree_layout(pa::tree_ctas(max_nodes, group), pa::tree_streams(max_nodes, group), head_dim).total;
 }
 
 int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tree, int64_t k_stride,
@@ -199,31 +183,31 @@ int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tre
     p.q_heads = num_q_heads;
     p.kv_heads = num_kv_heads;
     p.group = num_q_heads / num_kv_heads;
+    p.group_shift = p.group == 8 ? 3 : p.group >> 1;
     p.block_size = block_size;
     p.pool_rows = (int)rows;
     p.scale_log2 = scale * pa::kTreeLog2e;
-    p.chunks = pa::tree_chunks(max_nodes, p.group);
-    const int pt = max_seq_len > 0 ? pa::tree_partition(batch, num_q_heads, num_kv_heads, max_seq_len, max_nodes,
-                                                        partition_tokens)
-                                   : -1;
-    p.part_tokens = pt > 0 ? pt : (max_seq_len > 0 ? max_seq_len : 1);
-    p.num_parts = pt > 0 ? (max_seq_len + pt - 1) / pt : 1;
-    if (pt > 0) {
-        const pa::TreeLayout l = pa::tree_layout(num_rows, num_q_heads, head_dim, p.num_parts);
+    const int streams = pa::tree_streams(max_nodes, p.group), tile = pa::tree_tile(max_nodes, p.group);
+    const int share = pa::tree_share(max_seq_len, partition_tokens);
+    p.min_share = share > tile ? share / tile : 1;
+    if (share > 0) {
+        const pa::TreeLayout l = pa::tree_layout(pa::tree_ctas(max_nodes, p.group), streams, head_dim);
         if (!workspace || workspace_bytes < l.total || !pa::aligned16(workspace)) return PA_ERR_INVALID_ARG;
         p.part_o = static_cast<float *>(workspace);
         p.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + l.ml);
     }
-    if ((int64_t)p.chunks * p.num_parts > INT32_MAX || (int64_t)max_nodes * num_q_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    // row numbers and places of a unit are int32
+    if ((int64_t)max_nodes * num_q_heads > INT32_MAX / 2 || (int64_t)max_blocks_per_seq * block_size > INT32_MAX / 2)
+        return PA_ERR_UNSUPPORTED;
     pa::TreeMaps m;
     if (!pa::tree_rows_map(&m.q, q, q_stride, num_rows, num_q_heads, head_dim, p.group, pa::kTileM / p.group) ||
-        !pa::tree_rows_map(&m.kt, k_tree, k_stride, num_rows, num_kv_heads, head_dim, 1, pa::kTileN) ||
-        !pa::tree_rows_map(&m.vt, v_tree, v_stride, num_rows, num_kv_heads, head_dim, 1, pa::kTileN) ||
+        !pa::tree_rows_map(&m.kt, k_tree, k_stride, num_rows, num_kv_heads, head_dim, 1, tile) ||
+        !pa::tree_rows_map(&m.vt, v_tree, v_stride, num_rows, num_kv_heads, head_dim, 1, tile) ||
         !pa::tree_pool_map(&m.k, k_cache, rows, head_dim, block_size) ||
         !pa::tree_pool_map(&m.v, v_cache, rows, head_dim, block_size))
         return PA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (pa::tree_streams(max_nodes, p.group) == 2)
+    if (streams == 2)
         return head_dim == 128 ? pa::launch_tree<128, 2>(m, p, s) : pa::launch_tree<64, 2>(m, p, s);
     return head_dim == 128 ? pa::launch_tree<128, 1>(m, p, s) : pa::launch_tree<64, 1>(m, p, s);
 }

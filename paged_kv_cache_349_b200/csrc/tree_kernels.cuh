@@ -11,13 +11,16 @@
 //    of a kv head read the same keys, so (node, head of the group) pairs are the
 //    128 rows of one tcgen05.mma and each K and V byte leaves HBM once for up to
 //    128 * STREAMS query rows.
-//  * One CTA per (sequence, kv head, row chunk[, partition of the cache]).  A
-//    producer warp dereferences the block table and stages 64-token tiles of K
-//    and V (and, at the end, of the drafted rows) with TMA into one ring of tiles,
-//    in the order in which they are used: K0 K1 V0 K2 V1 ...
-//  * One warp issues the products.  S = Q K^T (bf16, fp32 accumulator in TMEM, two
-//    buffers, so that the scores of the next tile are ready while this one's
-//    softmax runs) and O += P V with P read from TMEM.
+//  * A unit of work is (sequence, kv head, row chunk): its tiles of cached tokens,
+//    then those of the drafted rows.  One CTA per slot of the GPU stays for the
+//    whole call and takes an equal share of all tiles, in order, so that neither
+//    the lengths nor the number of sequences leave SMs idle; a unit that is cut by
+//    a border between two CTAs leaves partial states for a second kernel.
+//  * A producer warp walks the units, dereferences the block table and stages the
+//    tiles of K and V with TMA into one ring, in the order in which they are used.
+//    It describes each tile (sequence, rows, valid tokens) in a ring of its own.
+//  * One thread issues the products.  S = Q K^T (bf16, fp32 accumulator in TMEM) and
+//    O += P V with P read from TMEM.
 //  * Four warps for each 128 rows run the softmax, a row to a thread: no shuffles.
 //    P replaces its scores in TMEM as bf16: 8 significant bits for each weight, as
 //    many as the values it multiplies have, and as the output keeps; the sum of the
@@ -26,6 +29,11 @@
 //    weight: O stays in TMEM and is rescaled a few times in a row's life instead of
 //    once a tile.  fp32 holds weights up to 2^8 as well as up to 1, and the
 //    quotient at the end does not depend on which reference was used.
+//  * STREAMS = 1 (up to 128 query rows, bound by HBM): 64-token tiles with two score
+//    buffers, two CTAs on an SM.  STREAMS = 2 (more rows, bound by the products and
+//    the exponentials): two groups of 128 rows share each K and V tile of 128 tokens
+//    and take turns on the tensor cores; an mma of N = 64 takes as long as one of
+//    N = 128 (65 cycles measured), so the longer tile halves their number.
 //  * What a row does not see has no part in it.  Scores are replaced, not added
 //    to; V rows past the sequence's end are zeroed in shared memory before they meet
 //    a weight of zero; non-finite values of drafted V rows (which some rows see and
@@ -39,42 +47,55 @@ namespace pa {
 namespace {
 
 constexpr float kTreeLog2e = 1.4426950408889634f;
-constexpr int kTileN = 64;         // tokens of one tile
 constexpr int kTileM = 128;        // query rows of one stream
 constexpr float kMaxRise = 8.0f;   // log2 of the largest weight before the reference moves
 
 template <int HEAD_DIM, int STREAMS>
 struct TreeCfg {
+    static constexpr int kTileN = STREAMS == 1 ? 64 : 128;     // tokens of one tile
+    static constexpr int kBufs = 128 / kTileN;                 // score buffers of a stream
     static constexpr int kBoxes = HEAD_DIM / 64;               // 128-byte wide column boxes
     static constexpr int kBoxBytes = kTileN * 128;             // one box of a K or V tile
     static constexpr int kTileBytes = kBoxes * kBoxBytes;
     static constexpr int kQBoxBytes = kTileM * 128;
     static constexpr int kQBytes = kBoxes * kQBoxBytes;        // one stream's queries
-    // Ring depth: two CTAs share an SM with one stream, one CTA has it alone with two.
-    static constexpr int kSlots = (STREAMS == 1 ? 4 : 8) * (HEAD_DIM == 64 ? 2 : 1);
+    static constexpr int kSlots = HEAD_DIM == 64 ? 8 : 4;      // ring depth
+    static constexpr int kMetas = 16;                          // tile descriptions
     static constexpr int kCtasPerSm = STREAMS == 1 ? 2 : 1;
     static constexpr int kSoftmaxWarps = 4 * STREAMS;
     static constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
-    // TMEM of one stream: two score buffers (P in the first half of each), then O.
-    static constexpr int kStreamCols = 2 * kTileN + 128;
+    // TMEM of one stream: the score buffers (P in the first half of each), then O.
+    static constexpr int kStreamCols = 128 + 128;
     static constexpr int kCols = STREAMS * kStreamCols;
-    static constexpr int kBars = 2 * kSlots + 1 + STREAMS * 6;
+    static constexpr int kBars = 2 * kSlots + 2 * kMetas + STREAMS * (2 * kBufs + 4) + 1;
     static constexpr int kDataBytes = STREAMS * kQBytes + kSlots * kTileBytes;
-    static constexpr int kSmemBytes = 1024 /* align slack */ + kDataBytes + kBars * 8 + 16;
+    // Each softmax warp turns its rows of the output into whole 64-byte pieces here.
+    static constexpr int kStageBytes = kSoftmaxWarps * 2048;
+    static constexpr int kTailBytes = kStageBytes + kMetas * 32 + kBars * 8 + 32 * 8 + 2 * 16 + 16;
+    static constexpr int kSmemBytes = 1024 /* align slack */ + kDataBytes + kTailBytes;
     static_assert(kCtasPerSm * kCols <= 512, "TMEM columns of an SM");
+    static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
+    // What a unit costs besides its tiles, and the shortest pieces worth cutting off, in tiles.
+    static constexpr int kUnitCost = 128 / kTileN;
+    static constexpr int kSnap = 128 / kTileN;
+};
+
+// Where a CTA's share begins: tile `tile` of unit `unit` of sequence `b` (b = batch: nowhere).
+struct TreeMark {
+    int b, unit, tile, pad;
 };
 
 struct TreeParams {
     uint16_t *out;             // [T, Hq, d] bf16
-    float *part_o;             // [T, Hq, parts, d]  (split)
-    float *part_ml;            // [T, Hq, parts, 2]  (split)
+    float *part_o;             // [CTAs, 2, rows of a unit, d]: states of units that are cut (NULL: none is)
+    float *part_ml;            // [CTAs, 2, rows of a unit, 2]
     const uint16_t *v_tree;
     const int32_t *tables, *lens, *cu, *masks;
     int32_t *err_flag;
     int64_t v_stride, num_blocks;
     int num_rows, batch, max_blocks, max_seq_len, max_nodes, words;
-    int q_heads, kv_heads, group, block_size;
-    int part_tokens, num_parts, chunks;
+    int q_heads, kv_heads, group, group_shift, block_size;
+    int min_share;             // tiles that a CTA takes at least
     int pool_rows;             // rows of the pools' tensor maps: a row outside of them reads as zeros
     float scale_log2;
 };
@@ -90,7 +111,7 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *m
 }
 
 // bf16 operands, fp32 accumulator of M = 128 rows and N columns; B transposed: stored [K, N]
-constexpr uint32_t tree_idesc(int n, bool b_transposed) {
+__host__ __device__ constexpr uint32_t tree_idesc(int n, bool b_transposed) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (b_transposed ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(kTileM >> 4) << 24);
 }
@@ -100,6 +121,12 @@ constexpr uint32_t tree_idesc(int n, bool b_transposed) {
 __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t box_bytes) {
     return (uint64_t)((saddr & 0x3ffffu) >> 4) | ((uint64_t)(box_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 
 __device__ __forceinline__ void umma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
@@ -136,19 +163,51 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// mbar_wait_bounded without reading the clock when the phase is already there.
+__device__ __forceinline__ bool tree_wait(uint64_t *bar, uint32_t parity, int32_t *flag) {
+    return mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, flag);
+}
 
 // A barrier of the softmax warps of one CTA that also ORs a predicate over them.
 template <int THREADS>
@@ -192,64 +251,179 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b) {
     return s;
 }
 
+// Row chunks of a sequence (units of one kv head) and the tiles of each.
+struct TreeUnits {
+    int chunks, ctx, tiles;
+};
+template <int HEAD_DIM, int STREAMS>
+__device__ __forceinline__ TreeUnits tree_units(const TreeParams &p, const TreeSeq &q) {
+    constexpr int N = TreeCfg<HEAD_DIM, STREAMS>::kTileN;
+    const int rows = STREAMS * kTileM;
+    TreeUnits u;
+    u.chunks = ((q.nodes << p.group_shift) + rows - 1) / rows;
+    u.ctx = (q.len + N - 1) / N;
+    u.tiles = u.ctx + (q.nodes + N - 1) / N;
+    return u;
+}
+
+// All tiles of the call, plus a fixed cost for each unit, form one line; `count` CTAs cut it into equal
+// parts.  A cut near a unit's end moves there (where units may not be cut, every cut does).
+struct TreeLine {
+    int64_t total, before, mine;  // this thread's sequences [b0, b1) lie at [before, before + mine)
+    int b0, b1, count, step, rest;
+};
+
+template <int HEAD_DIM, int STREAMS, int THREADS>
+__device__ __forceinline__ TreeLine tree_line(const TreeParams &p, int ctas, int64_t *scan, bool report) {
+    using C = TreeCfg<HEAD_DIM, STREAMS>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = p.batch <= THREADS ? 1 : (p.batch + THREADS - 1) / THREADS;
+    TreeLine n;
+    n.b0 = min((int)threadIdx.x * per, p.batch);
+    n.b1 = min(n.b0 + per, p.batch);
+    n.mine = 0;
+    for (int b = n.b0; b < n.b1; ++b) {
+        const TreeSeq seq = tree_seq(p, b);
+        if (seq.bad && report) raise_flag(p.err_flag, PA_FLAG_BAD_LEN);
+        const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, seq);
+        n.mine += (int64_t)(u.chunks * p.kv_heads) * (u.tiles + C::kUnitCost);
+    }
+    int64_t incl = n.mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += up;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    n.before = incl - n.mine;
+    n.total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) n.before += scan[w];
+        n.total += scan[w];
+    }
+    // Shares of at least min_share tiles, so that neighbouring cuts never coincide inside a unit.
+    if (n.total <= INT32_MAX) {
+        n.count = max(1, min(ctas, (int)n.total / p.min_share));
+        n.step = (int)n.total / n.count;
+        n.rest = (int)n.total - n.step * n.count;
+    } else {
+        n.count = ctas;
+        n.step = -1;
+        n.rest = 0;
+    }
+    return n;
+}
+
+// Where cut i lies on the line.
+__device__ __forceinline__ int64_t tree_cut(const TreeLine &n, int i) {
+    if (i >= n.count) return n.total;
+    return n.step >= 0 ? (int64_t)n.step * i + n.rest * i / n.count : n.total / n.count * i;
+}
+
+// The tile at which a cut `at` into a sequence's units falls, as (unit, tile).
+template <int HEAD_DIM, int STREAMS>
+__device__ __forceinline__ TreeMark tree_mark(const TreeParams &p, const TreeUnits &u, int b, int64_t at) {
+    using C = TreeCfg<HEAD_DIM, STREAMS>;
+    const int weight = u.tiles + C::kUnitCost;
+    TreeMark m{b, at <= INT32_MAX ? (int)at / weight : (int)(at / weight), 0, 0};
+    const int tile = (int)(at - (int64_t)m.unit * weight) - C::kUnitCost;
+    if (p.part_o ? tile > u.tiles - C::kSnap : 2 * tile >= u.tiles)
+        ++m.unit;
+    else if (p.part_o && tile >= C::kSnap)
+        m.tile = tile;
+    return m;
+}
+
+// The marks of cuts i and i + 1.  Every CTA computes the same cuts from the lengths alone.
+template <int HEAD_DIM, int STREAMS, int THREADS>
+__device__ __forceinline__ void tree_marks(const TreeParams &p, int ctas, int i, int64_t *scan, TreeMark *mark, bool report) {
+    using C = TreeCfg<HEAD_DIM, STREAMS>;
+    const TreeLine n = tree_line<HEAD_DIM, STREAMS, THREADS>(p, ctas, scan, report);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        int64_t at = tree_cut(n, i + k);
+        if (threadIdx.x == 0 && at >= n.total) mark[k] = TreeMark{p.batch, 0, 0, 0};
+        at -= n.before;
+        if (at < 0 || at >= n.mine) continue;
+        for (int b = n.b0; b < n.b1; ++b) {
+            const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, tree_seq(p, b));
+            const int64_t weight = (int64_t)(u.chunks * p.kv_heads) * (u.tiles + C::kUnitCost);
+            if (at < weight) {
+                mark[k] = tree_mark<HEAD_DIM, STREAMS>(p, u, b, at);
+                break;
+            }
+            at -= weight;
+        }
+    }
+    __syncthreads();
+}
+
+// One tile, as the producer describes it to the other warps.
+enum { kFirst = 1, kLast = 2, kTree = 4, kTwo = 8, kEnd = 16, kPlain = 32, kHoles = 8 /* shift of 16 page bits */ };
+struct __align__(16) TileMeta {
+    int flags;   // first / last of its piece, drafted rows, both streams have rows, no tile, seen by all rows
+                 // as a whole; pages with a bad block
+    int valid;   // tokens (or nodes) in it
+    int start;   // first token (or node)
+    int dest;    // -1: the piece is a whole unit; else its partial state's place
+    int b, first, nodes;
+    int place;   // node0 * kv_heads + kv head
+};
+
 template <int HEAD_DIM, int STREAMS>
 __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<HEAD_DIM, STREAMS>::kCtasPerSm)
     tree_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap kt_map,
                 const __grid_constant__ CUtensorMap vt_map, const TreeParams p) {
     using C = TreeCfg<HEAD_DIM, STREAMS>;
+    constexpr int kTileN = C::kTileN, kBufs = C::kBufs, kSlots = C::kSlots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     uint8_t *ring = smem + STREAMS * C::kQBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kDataBytes);
-    uint64_t *empty = full + C::kSlots;
-    uint64_t *q_full = empty + C::kSlots;
-    uint64_t *s_full = q_full + 1;              // [stream][buffer]: scores are in TMEM
-    uint64_t *p_full = s_full + 2 * STREAMS;    // [stream][buffer]: weights are in TMEM
-    uint64_t *pv_done = p_full + 2 * STREAMS;   // [stream]: a tile has been added to O
-    uint64_t *o_done = pv_done + STREAMS;       // [stream]: all of them have
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_done + STREAMS);
-    volatile int *tree_dirty = reinterpret_cast<volatile int *>(tmem_slot + 1);  // drafted V holds NaN or infinities
+    uint8_t *stage = smem + C::kDataBytes;
+    TileMeta *meta = reinterpret_cast<TileMeta *>(stage + C::kStageBytes);
+    TreeMark *mark = reinterpret_cast<TreeMark *>(meta + C::kMetas);  // [2]
+    int64_t *scan = reinterpret_cast<int64_t *>(mark + 2);            // [32]
+    uint64_t *full = reinterpret_cast<uint64_t *>(scan + 32);
+    uint64_t *empty = full + kSlots;
+    uint64_t *meta_full = empty + kSlots;
+    uint64_t *meta_free = meta_full + C::kMetas;  // every softmax warp is done with the description
+    uint64_t *s_full = meta_free + C::kMetas;     // [stream][buffer]: scores are in TMEM
+    uint64_t *p_full = s_full + kBufs * STREAMS;  // [stream][buffer]: weights are in TMEM
+    uint64_t *q_full = p_full + kBufs * STREAMS;  // [stream]: the piece's queries are in shared memory
+    uint64_t *pv_done = q_full + STREAMS;         // [stream]: a tile has been added to O
+    uint64_t *o_done = pv_done + STREAMS;         // [stream]: a piece's last tile has
+    uint64_t *o_free = o_done + STREAMS;          // [stream]: a piece's O has been read
+    uint64_t *drained = o_free + STREAMS;         // every product has completed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int chunk = blockIdx.x % p.chunks, part = blockIdx.x / p.chunks;
-    const int h = blockIdx.y, b = blockIdx.z;
-    const TreeSeq seq = tree_seq(p, b);
-    if (seq.bad && threadIdx.x == 0 && blockIdx.x == 0 && h == 0) raise_flag(p.err_flag, PA_FLAG_BAD_LEN);
-
-    // ---- the work: rows [row0, ...) of the sequence, tokens [t0, t1) and (first partition) the tree ----
     const int G = p.group;
-    const int tile_nodes = kTileM / G;
-    const int node0 = chunk * STREAMS * tile_nodes;
-    if (node0 >= seq.nodes) return;
-    const int t0 = part * p.part_tokens;
-    const int t1 = min(seq.len, t0 + p.part_tokens);
-    const int n_ctx = t1 > t0 ? (t1 - t0 + kTileN - 1) / kTileN : 0;
-    // a chain's rows see no node after their own
-    const int reach = p.masks ? seq.nodes : min(seq.nodes, node0 + STREAMS * tile_nodes);
-    const int n_tree = part == 0 ? (reach + kTileN - 1) / kTileN : 0;
-    const int n = n_ctx + n_tree;
-    if (n == 0) return;
-    const int streams = STREAMS == 2 && node0 + tile_nodes < seq.nodes ? 2 : 1;
-    const bool whole = seq.len <= p.part_tokens;  // no other partition: the output is written here
-    if (p.num_parts > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tile_nodes = kTileM / G;  // nodes of one stream's rows
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kSlots; ++s) {
+        for (int s = 0; s < kSlots; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
         }
-        mbar_init(q_full, 1);
-        for (int s = 0; s < 2 * STREAMS; ++s) {
+        for (int s = 0; s < C::kMetas; ++s) {
+            mbar_init(meta_full + s, 1);
+            mbar_init(meta_free + s, C::kSoftmaxWarps);
+        }
+        for (int s = 0; s < kBufs * STREAMS; ++s) {
             mbar_init(s_full + s, 1);
             mbar_init(p_full + s, 4);
         }
         for (int s = 0; s < STREAMS; ++s) {
+            mbar_init(q_full + s, 1);
             mbar_init(pv_done + s, 1);
             mbar_init(o_done + s, 1);
+            mbar_init(o_free + s, 4);
         }
-        *tree_dirty = 0;
+        mbar_init(drained, 1);
         fence_mbar_init();
     }
     if (warp == C::kSoftmaxWarps + 1) {
@@ -257,335 +431,482 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         tmem_relinquish();
         tc_fence_before();
     }
-    __syncthreads();
+    tree_marks<HEAD_DIM, STREAMS, C::kThreads>(p, gridDim.x, blockIdx.x, scan, mark, blockIdx.x == 0);  // synchronises
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    if (p.part_o) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // Place in the ring of K and V of tile j: K0 K1 V0 K2 V1 ... V(n-2) V(n-1).
-    auto k_item = [](int j) { return j + (j > 1 ? j - 1 : 0); };
-    auto v_item = [&](int j) { return j + (j + 2 < n ? j + 2 : n); };
+    // The tiles of this CTA are numbered through all its pieces.  Items of the ring, in their order:
+    // K of the first kBufs tiles, then V(0) K(kBufs) V(1) K(kBufs + 1) ...
+    auto k_item = [](int t) { return t < kBufs ? t : 2 * t - kBufs + 1; };
+    auto v_item = [](int t) { return 2 * t + kBufs; };
 
     if (warp == C::kSoftmaxWarps) {
-        // ---------------- producer: block-table dereference + TMA ----------------
-        const int pages = kTileN / p.block_size;          // of one tile
+        // ---------------- producer: units, block-table dereference, TMA ----------------
+        const int pages = kTileN / p.block_size;  // of one tile
         const int page = lane / C::kBoxes, box = lane % C::kBoxes;
-        const int32_t *table = p.tables + (int64_t)b * p.max_blocks;
-        const int last = (t1 + p.block_size - 1) / p.block_size;  // blocks of the range end here
-        // Block id of this lane's page of tile j: -1 past the range, -2 a bad id.
-        auto entry = [&](int j) -> int {
-            if (j >= n_ctx || page >= pages) return -1;
-            const int at = t0 / p.block_size + j * pages + page;
-            if (at >= last) return -1;
-            const int id = __ldg(table + at);
-            return id < 0 || id >= p.num_blocks ? -2 : id;
-        };
-        if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, streams * C::kQBytes);
-            for (int s = 0; s < streams; ++s)
-                for (int x = 0; x < C::kBoxes; ++x)
-                    tma_load_3d(smem + s * C::kQBytes + x * C::kQBoxBytes, &q_map, x * 64, h * G,
-                                seq.first + node0 + s * tile_nodes, q_full);
+        const TreeMark end = mark[1];
+        // K and V are read once by one row chunk, again soon (from L2) by the others
+        const uint64_t policy = p.max_nodes > STREAMS * tile_nodes ? l2_policy_evict_normal() : l2_policy_evict_first();
+
+        // The walk over units and their tiles, from this CTA's mark to the next one's.  What stays the same
+        // within a piece is worked out when the piece begins.
+        TreeMark cur = mark[0];
+        TreeSeq seq{}, ahead{};
+        TreeUnits of{};
+        if (cur.b < p.batch) {
+            seq = tree_seq(p, cur.b);
+            of = tree_units<HEAD_DIM, STREAMS>(p, seq);
+            if (cur.b + 1 < p.batch) ahead = tree_seq(p, cur.b + 1);
         }
-        const uint64_t policy = l2_policy_evict_first();
-        // entries of tiles v, v + 1 (the K beside it), and two more that are on their way
-        int e0 = entry(0), e1 = entry(1), e2 = entry(2), e3 = entry(3);
-        int v = 0, issued = 0;
-        for (int it = 0; it < 2 * n; ++it) {
-            const int slot = it % C::kSlots;
-            bool ok = true;
-            if (it >= C::kSlots) ok = mbar_wait_bounded(empty + slot, (it / C::kSlots - 1) & 1, p.err_flag);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            const int ahead = (it + 1) >> 1;
-            const bool is_k = it == 0 || ((it & 1) && ahead < n);
-            const int j = is_k ? ahead : v;
-            const int id = is_k && it > 0 ? e1 : e0;
-            uint8_t *dst = ring + slot * C::kTileBytes;
-            if (j < n_ctx) {
-                if (id == -2 && is_k && box == 0) raise_flag(p.err_flag, PA_FLAG_BAD_BLOCK);
-                const int loads = __popc(__ballot_sync(0xffffffffu, id != -1));
-                if (lane == 0) mbar_arrive_expect_tx(full + slot, loads * p.block_size * 128);
-                __syncwarp();
-                if (id != -1) {
-                    // a bad block reads as zeros (a row outside of the map)
-                    const int row = id == -2 ? p.pool_rows : (int)(((int64_t)id * p.kv_heads + h) * p.block_size);
-                    tma_load_2d(dst + box * C::kBoxBytes + page * p.block_size * 128, is_k ? &k_map : &v_map, box * 64,
-                                row, full + slot, policy);
+        // A tile to be loaded: this lane loads column box `box` of block `id` of it, if it has a page at all.
+        struct Tile {
+            int flags, start, valid, id;
+            bool mine;
+            int dest, b, first, nodes, place, h;  // the piece's
+        };
+        Tile piece{};
+        int stop = 0;       // the piece's tiles end here
+        bool fresh = true;  // a piece begins
+        const int32_t *entries = nullptr;  // this lane's page of the sequence's first tile
+        auto next_tile = [&]() -> Tile {
+            if (fresh) {
+                piece.flags = kEnd;
+                piece.mine = false;
+                for (;;) {
+                    const bool more = cur.b != end.b        ? cur.b < end.b
+                                      : cur.unit != end.unit ? cur.unit < end.unit
+                                                             : cur.tile < end.tile;
+                    if (!more) return piece;
+                    if (cur.unit < of.chunks * p.kv_heads) break;
+                    ++cur.b;  // on to the next sequence
+                    cur.unit = cur.tile = of.chunks = 0;
+                    seq = ahead;
+                    if (cur.b < p.batch) of = tree_units<HEAD_DIM, STREAMS>(p, seq);
+                    if (cur.b + 1 < p.batch) ahead = tree_seq(p, cur.b + 1);
                 }
+                piece.h = of.chunks == 1 ? cur.unit : cur.unit / of.chunks;
+                const int node0 = (cur.unit - piece.h * of.chunks) * (STREAMS * tile_nodes);
+                piece.place = node0 * p.kv_heads + piece.h;
+                stop = cur.b == end.b && cur.unit == end.unit ? end.tile : of.tiles;
+                piece.dest = cur.tile == 0 && stop == of.tiles ? -1 : 2 * (int)blockIdx.x + (cur.tile == 0);
+                piece.b = cur.b;
+                piece.first = seq.first;
+                piece.nodes = seq.nodes;
+                piece.flags = kFirst | (STREAMS == 2 && node0 + tile_nodes < seq.nodes ? kTwo : 0);
+                entries = p.tables + (int64_t)cur.b * p.max_blocks + page;
+            }
+            Tile t = piece;
+            piece.flags &= ~kFirst;
+            if (cur.tile < of.ctx) {
+                t.start = cur.tile * kTileN;
+                t.valid = min(kTileN, seq.len - t.start);
+                t.mine = page < pages && t.start + page * p.block_size < seq.len;
+                if (t.mine) t.id = __ldg(entries + cur.tile * pages);
+                if (t.valid == kTileN) t.flags |= kPlain;
             } else {
+                t.flags |= kTree;
+                t.start = (cur.tile - of.ctx) * kTileN;
+                t.valid = min(kTileN, seq.nodes - t.start);
+            }
+            fresh = ++cur.tile == stop;
+            if (fresh) {
+                t.flags |= kLast;
+                if (stop == of.tiles) {
+                    ++cur.unit;
+                    cur.tile = 0;
+                }
+            }
+            return t;
+        };
+        int landed = -1;  // lane s: the last item loaded into slot s
+        auto take_slot = [&](int it) {
+            bool ok = true;
+            if (it >= kSlots) ok = tree_wait(empty + it % kSlots, (it / kSlots - 1) & 1, p.err_flag);
+            return (bool)__all_sync(0xffffffffu, ok);
+        };
+        auto load = [&](const Tile &t, bool is_k, int it) {
+            const int slot = it % kSlots;
+            uint8_t *dst = ring + slot * C::kTileBytes;
+            if (lane == slot) landed = it;
+            if (t.flags & kTree) {
                 if (lane == 0) {
                     mbar_arrive_expect_tx(full + slot, C::kTileBytes);
                     for (int x = 0; x < C::kBoxes; ++x)
-                        tma_load_3d(dst + x * C::kBoxBytes, is_k ? &kt_map : &vt_map, x * 64, h,
-                                    seq.first + (j - n_ctx) * kTileN, full + slot);
+                        tma_load_3d(dst + x * C::kBoxBytes, is_k ? &kt_map : &vt_map, x * 64, t.h, t.first + t.start,
+                                    full + slot);
                 }
+                return;
             }
-            if (!is_k) {
-                ++v;
-                e0 = e1;
-                e1 = e2;
-                e2 = e3;
-                e3 = entry(v + 3);
-            }
-            issued = it + 1;
-        }
-        // Every copy has landed before the CTA ends (they have, unless a wait ran out).
-        for (int it = issued > C::kSlots ? issued - C::kSlots : 0; it < issued; ++it)
-            if (!mbar_wait_bounded(full + it % C::kSlots, (it / C::kSlots) & 1, p.err_flag)) break;
-        mbar_wait_bounded(q_full, 0, p.err_flag);
-    } else if (warp == C::kSoftmaxWarps + 1) {
-        // ---------------- products ----------------
-        const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
-        constexpr uint32_t kQkDesc = tree_idesc(kTileN, false), kPvDesc = tree_idesc(HEAD_DIM, true);
-        auto all_ok = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
-        auto wait_item = [&](int it) {
-            return all_ok(mbar_wait_bounded(full + it % C::kSlots, (it / C::kSlots) & 1, p.err_flag));
-        };
-        // S[stream][j & 1] = Q K_j^T
-        auto scores = [&](int j, int s) {
-            const uint32_t k0 = ring_addr + (k_item(j) % C::kSlots) * C::kTileBytes;
-            const uint32_t d = tmem + s * C::kStreamCols + (j & 1) * kTileN;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < HEAD_DIM / 16; ++i)
-                umma_bf16_ss(d, umma_desc_k_sw128(q_addr + s * C::kQBytes + (i >> 2) * C::kQBoxBytes + (i & 3) * 32),
-                             umma_desc_k_sw128(k0 + (i >> 2) * C::kBoxBytes + (i & 3) * 32), kQkDesc, i > 0);
-            umma_commit(s_full + 2 * s + (j & 1));
-        };
-        bool ok = all_ok(mbar_wait_bounded(q_full, 0, p.err_flag));
-        for (int j = 0; ok && j < min(2, n); ++j) {
-            ok = wait_item(k_item(j));
-            if (ok && lane == 0) {
-                for (int s = 0; s < streams; ++s) scores(j, s);
-                umma_commit(empty + k_item(j) % C::kSlots);
-            }
+            const int loads = __popc(__ballot_sync(0xffffffffu, t.mine));
+            if (lane == 0) mbar_arrive_expect_tx(full + slot, loads * p.block_size * 128);
             __syncwarp();
-        }
-        for (int j = 0; ok && j < n; ++j) {
-            const int slot = v_item(j) % C::kSlots;
-            if (!(ok = wait_item(v_item(j)))) break;
-            const uint32_t v0 = ring_addr + slot * C::kTileBytes;
-            const int rows = j < n_ctx ? t1 - t0 - j * kTileN : reach - (j - n_ctx) * kTileN;
-            if (rows < kTileN) {  // rows past the end: zeros, whatever the ring held
-                for (int x = lane; x < (kTileN - rows) * 8 * C::kBoxes; x += 32) {
-                    const int bx = x / ((kTileN - rows) * 8), y = x - bx * (kTileN - rows) * 8;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + bx * C::kBoxBytes +
-                                                                                   rows * 128 + y * 16),
-                                 "r"(0u)
-                                 : "memory");
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
+            if (t.mine) {
+                // a bad block reads as zeros (a row outside of the map)
+                const bool bad = t.id < 0 || t.id >= p.num_blocks;
+                const int row = bad ? p.pool_rows : (int)(((int64_t)t.id * p.kv_heads + t.h) * p.block_size);
+                tma_load_2d(dst + box * C::kBoxBytes + page * p.block_size * 128, is_k ? &k_map : &v_map, box * 64, row,
+                            full + slot, policy);
             }
-            for (int s = 0; ok && s < streams; ++s) {
-                ok = all_ok(mbar_wait_bounded(p_full + 2 * s + (j & 1), (j >> 1) & 1, p.err_flag));
-                if (!ok) break;
-                if (s == 0 && j >= n_ctx && *tree_dirty) {
-                    for (int x = lane; x < C::kTileBytes / 16; x += 32) {
-                        const uint4 w = lds128(v0 + x * 16);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(v0 + x * 16), "r"(finite2(w.x)),
-                                     "r"(finite2(w.y)), "r"(finite2(w.z)), "r"(finite2(w.w))
-                                     : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+        };
+        // Tiles are drawn ahead of their loads, so that table entries are there when they are needed.
+        Tile t0 = next_tile(), t1 = next_tile(), older = t0;
+        int n = INT_MAX;  // tiles of this CTA, once known
+        for (int t = 0;; ++t) {
+            if (n == INT_MAX) {
+                if (!take_slot(k_item(t))) break;
+                const uint32_t holes = __ballot_sync(0xffffffffu, t0.mine && box == 0 && (t0.id < 0 || t0.id >= p.num_blocks));
+                if (holes) {
+                    if (lane == 0) raise_flag(p.err_flag, PA_FLAG_BAD_BLOCK);
+                    for (int x = 0; x < pages; ++x)
+                        if ((holes >> (x * C::kBoxes)) & 1) t0.flags |= 1 << (kHoles + x);
+                    t0.flags &= ~kPlain;
                 }
+                const int mt = t % C::kMetas;
+                const bool free = t < C::kMetas || tree_wait(meta_free + mt, (t / C::kMetas - 1) & 1, p.err_flag);
+                if (!__all_sync(0xffffffffu, free)) break;
                 if (lane == 0) {
-                    tc_fence_after();
-                    const uint32_t base = tmem + s * C::kStreamCols;
-#pragma unroll
-                    for (int i = 0; i < kTileN / 16; ++i)
-                        umma_bf16_ts(base + 2 * kTileN, base + (j & 1) * kTileN + 8 * i,
-                                     umma_desc_mn_sw128(v0 + i * 2048, C::kBoxBytes), kPvDesc, j > 0 || i > 0);
-                    umma_commit(j + 1 < n ? pv_done + s : o_done + s);
+                    meta[mt] = TileMeta{t0.flags, t0.valid, t0.start, t0.dest, t0.b, t0.first, t0.nodes, t0.place};
+                    mbar_arrive(meta_full + mt);
                 }
-                __syncwarp();
+                if (t0.flags & kEnd)
+                    n = t;
+                else
+                    load(t0, true, k_item(t));
             }
-            if (!ok) break;
-            if (lane == 0) umma_commit(empty + slot);
-            if (j + 2 < n) {
-                if (!(ok = wait_item(k_item(j + 2)))) break;
-                for (int s = 0; s < streams; ++s) {
-                    // the new scores take the place of P_j: its product has to be done
-                    ok = all_ok(mbar_wait_bounded(pv_done + s, j & 1, p.err_flag));
-                    if (!ok) break;
-                    if (lane == 0) scores(j + 2, s);
-                    __syncwarp();
-                }
-                if (lane == 0) umma_commit(empty + k_item(j + 2) % C::kSlots);
+            const int u = t - (kBufs - 1);  // the tile whose V comes next
+            if (u >= n) break;
+            if (u >= 0) {
+                if (!take_slot(v_item(u))) break;
+                load(kBufs == 1 ? t0 : older, false, v_item(u));
             }
-            __syncwarp();
+            older = t0;
+            t0 = t1;
+            t1 = next_tile();
         }
-        // Every product has completed before TMEM is freed.
-        for (int s = 0; ok && s < streams; ++s) ok = mbar_wait_bounded(o_done + s, 0, p.err_flag);
-    } else if (warp < 4 * streams) {
+        // Every copy has landed before the CTA ends (it has, unless a wait ran out).
+        if (lane < kSlots && landed >= 0) mbar_wait_bounded(full + lane, (landed / kSlots) & 1, p.err_flag);
+    } else if (warp == C::kSoftmaxWarps + 1) {
+        // ---------------- products, issued by one thread ----------------
+        if (lane == 0) {
+            constexpr uint32_t kQkDesc = tree_idesc(kTileN, false), kPvDesc = tree_idesc(HEAD_DIM, true);
+            // Descriptors of the queries and of ring slot 0; a step through the operand or to another
+            // slot adds to the start address (16-byte units), which never carries out of its field.
+            const uint64_t q_desc = umma_desc_k_sw128(smem_addr(smem));
+            const uint64_t k_desc = umma_desc_k_sw128(smem_addr(ring));
+            const uint64_t v_desc = umma_desc_mn_sw128(smem_addr(ring), C::kBoxBytes);
+            // per stream: tiles whose scores / products were issued, and their pieces
+            int scored[STREAMS] = {}, added[STREAMS] = {}, pieces_q[STREAMS] = {}, pieces_o[STREAMS] = {};
+            int queue[kBufs] = {};  // flags of the tiles between the two
+            auto wait_item = [&](int it) { return tree_wait(full + it % kSlots, (it / kSlots) & 1, p.err_flag); };
+            bool ok = true, over = false;
+            for (int t = 0; ok; ++t) {
+                // O += P V of tile t - kBufs, then S = Q K^T of tile t, one stream after the other: while
+                // one waits for its softmax, the other has the tensor cores
+                const int f_pv = t >= kBufs ? queue[0] : 0;
+                const bool pv = t >= kBufs && !(f_pv & kEnd);
+                if (t >= kBufs && !pv) break;
+                int f_qk = kEnd;
+                uint64_t vd = 0, kd = 0;
+                if (pv) {
+                    if (!(ok = wait_item(v_item(t - kBufs)))) break;
+                    vd = v_desc + (uint32_t)(v_item(t - kBufs) % kSlots * (C::kTileBytes / 16));
+                }
+#pragma unroll
+                for (int s = 0; s < STREAMS; ++s) {
+                    if (ok && pv && (s == 0 || (f_pv & kTwo))) {
+                        const int g = added[s]++;
+                        ok = tree_wait(p_full + kBufs * s + g % kBufs, (g / kBufs) & 1, p.err_flag);
+                        // a new piece overwrites O: the last one's has to have been read
+                        if (ok && (f_pv & kFirst) && pieces_o[s]++ > 0) ok = tree_wait(o_free + s, pieces_o[s] & 1, p.err_flag);
+                        if (ok) {
+                            tc_fence_after();
+                            const uint32_t base = tmem + s * C::kStreamCols;
+                            const uint32_t a = base + g % kBufs * kTileN;
+#pragma unroll
+                            for (int i = 0; i < kTileN / 16; ++i)
+                                umma_bf16_ts(base + 128, a + 8 * i, vd + i * (2048 / 16), kPvDesc, !(f_pv & kFirst) || i > 0);
+                            umma_commit(pv_done + s);
+                            if (f_pv & kLast) umma_commit(o_done + s);
+                        }
+                    }
+                    if (s == 0 && ok && !over) {
+                        ok = tree_wait(meta_full + t % C::kMetas, (t / C::kMetas) & 1, p.err_flag);
+                        if (ok) f_qk = *const_cast<volatile int *>(&meta[t % C::kMetas].flags);
+                        over = f_qk & kEnd;
+                        if (ok && !over) {
+                            ok = wait_item(k_item(t));
+                            kd = k_desc + (uint32_t)(k_item(t) % kSlots * (C::kTileBytes / 16));
+                        }
+                    }
+                    if (ok && !over && (s == 0 || (f_qk & kTwo))) {
+                        if (f_qk & kFirst) ok = tree_wait(q_full + s, pieces_q[s]++ & 1, p.err_flag);
+                        const int g = scored[s]++;
+                        // the new scores take the place of an earlier tile's P: its product has to be done
+                        if (ok && g >= kBufs) ok = tree_wait(pv_done + s, (g - kBufs) & 1, p.err_flag);
+                        if (ok) {
+                            tc_fence_after();
+                            const uint64_t qd = q_desc + (uint32_t)(s * (C::kQBytes / 16));
+                            const uint32_t d = tmem + s * C::kStreamCols + g % kBufs * kTileN;
+#pragma unroll
+                            for (int i = 0; i < HEAD_DIM / 16; ++i)
+                                umma_bf16_ss(d, qd + ((i >> 2) * C::kQBoxBytes + (i & 3) * 32) / 16,
+                                             kd + ((i >> 2) * C::kBoxBytes + (i & 3) * 32) / 16, kQkDesc, i > 0);
+                            umma_commit(s_full + kBufs * s + g % kBufs);
+                        }
+                    }
+                }
+                if (!ok) break;
+                if (pv) umma_commit(empty + v_item(t - kBufs) % kSlots);
+                if (!over) umma_commit(empty + k_item(t) % kSlots);
+#pragma unroll
+                for (int x = 0; x + 1 < kBufs; ++x) queue[x] = queue[x + 1];
+                queue[kBufs - 1] = f_qk;
+            }
+            umma_commit(drained);
+            mbar_wait_bounded(drained, 0, p.err_flag);
+        }
+    } else {
         // ---------------- softmax: one row to a thread ----------------
         const int s = warp >> 2;
         const int r = threadIdx.x & (kTileM - 1);
-        const int node = node0 + s * tile_nodes + r / G;
-        const bool live = node < seq.nodes;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t base = tmem + s * C::kStreamCols + lanes;
-        const uint32_t o_addr = base + 2 * kTileN;
-
-        // While the first tiles are on their way: do drafted V rows hold values that must not meet a
-        // weight of zero, and does the block table name blocks that are not there?
-        bool dirty = false, holes = false;
-        constexpr int kVecs = HEAD_DIM / 8;
-        if (n_tree) {
-            for (int x = threadIdx.x; x < reach * kVecs; x += 128 * streams) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.v_tree + (int64_t)(seq.first + x / kVecs) * p.v_stride +
-                                                                      h * HEAD_DIM) + x % kVecs);
-                dirty |= not_finite2(w.x) || not_finite2(w.y) || not_finite2(w.z) || not_finite2(w.w);
-            }
-        }
-        const int32_t *table = p.tables + (int64_t)b * p.max_blocks;
-        for (int at = t0 / p.block_size + threadIdx.x; at < (t1 + p.block_size - 1) / p.block_size; at += 128 * streams) {
-            const int id = __ldg(table + at);
-            holes |= id < 0 || id >= p.num_blocks;
-        }
-        if (streams == STREAMS) {
-            dirty = softmax_any<128 * STREAMS>(dirty);
-            holes = softmax_any<128 * STREAMS>(holes);
-        } else {
-            dirty = softmax_any<128>(dirty);
-            holes = softmax_any<128>(holes);
-        }
-        if (dirty && threadIdx.x == 0) *tree_dirty = 1;  // before this thread's first arrival on p_full
-
+        const uint32_t base = tmem + s * C::kStreamCols + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t o_addr = base + 128;
         // a negative scale turns the order of the scores around; a scale of 0 must not meet -inf
         const bool flip = p.scale_log2 < 0.f;
         const float c = p.scale_log2 == 0.f ? 1e-30f : fabsf(p.scale_log2);
         const float rise = kMaxRise / c;
+
+        // One thread of each stream loads its queries: the first piece's at once, the next one's when the
+        // last scores of a piece are there, while their softmax and the piece's output are still to come.
+        int q_loads = 0;
+        auto load_queries = [&](int t) {
+            if (!tree_wait(meta_full + t % C::kMetas, (t / C::kMetas) & 1, p.err_flag)) return;
+            const volatile TileMeta &m = meta[t % C::kMetas];
+            const int f = m.flags, place = m.place, first = m.first;
+            if ((f & kEnd) || (s == 1 && !(f & kTwo))) return;
+            mbar_arrive_expect_tx(q_full + s, C::kQBytes);
+            for (int x = 0; x < C::kBoxes; ++x)
+                tma_load_3d(smem + s * C::kQBytes + x * C::kQBoxBytes, &q_map, x * 64, place % p.kv_heads * G,
+                            first + place / p.kv_heads + s * tile_nodes, q_full + s);
+            ++q_loads;
+        };
+        if ((warp & 3) == 0 && lane == 0) load_queries(0);
+
+        constexpr int kWords = kTileN / 32;
+        int node = 0, h = 0, g = 0, pieces = 0;  // g: tiles of this stream so far
+        bool live = false, seen = false, dirty = false;
+        uint32_t tree_bits[kWords] = {};  // the row's mask of the first drafted tile
         float m = -INFINITY, l = 0.f;
-        bool seen = false;
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            // the tokens of the tile that this row sees
-            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-            if (j < n_ctx) {
-                const int left = t1 - t0 - j * kTileN;
-                if (left < kTileN) {
-                    see[0] = left >= 32 ? 0xffffffffu : (1u << left) - 1;
-                    see[1] = left <= 32 ? 0u : (1u << (left - 32)) - 1;
-                }
-                if (holes) {
-                    const int at = (t0 + j * kTileN) / p.block_size;
-                    for (int x = 0; x * p.block_size < min(left, kTileN); ++x) {
-                        const int id = __ldg(table + at + x);
-                        if (id < 0 || id >= p.num_blocks)
-                            for (int t = x * p.block_size; t < (x + 1) * p.block_size; ++t) see[t >> 5] &= ~(1u << (t & 31));
-                    }
-                }
-            } else {
-                const int at = (j - n_ctx) * kTileN;
+        for (int t = 0;; ++t) {
+            const int mt = t % C::kMetas;
+            ok = tree_wait(meta_full + mt, (t / C::kMetas) & 1, p.err_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const int flags = meta[mt].flags;
+            if (flags & kEnd) break;
+            if (s == 1 && !(flags & kTwo)) {
+                if ((flags & kLast) && (warp & 3) == 0 && lane == 0) load_queries(t + 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(meta_free + mt);
+                continue;
+            }
+            if (flags & kFirst) {
+                h = meta[mt].place % p.kv_heads;
+                node = meta[mt].place / p.kv_heads + s * tile_nodes + (r >> p.group_shift);
+                live = node < meta[mt].nodes;
+                seen = dirty = false;
+                m = -INFINITY;
+                l = 0.f;
+                if (p.masks && live) {  // needed at the end of the piece: fetched now
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int first = at + 32 * w;  // the word's first node
-                    uint32_t bits = 0u;
-                    if (live && first < seq.nodes) {
-                        if (p.masks)
-                            bits = (uint32_t)__ldg(p.masks + (int64_t)(seq.first + node) * p.words + (first >> 5));
-                        else
-                            bits = node < first ? 0u : node - first >= 31 ? 0xffffffffu : (2u << (node - first)) - 1;
-                        if (seq.nodes - first < 32) bits &= (1u << (seq.nodes - first)) - 1;
-                    }
-                    see[w] = bits;
+                    for (int w = 0; w < kWords; ++w)
+                        tree_bits[w] = w < p.words ? (uint32_t)__ldg(p.masks + (int64_t)(meta[mt].first + node) * p.words + w) : 0u;
                 }
             }
-            seen |= (see[0] | see[1]) != 0;
-
-            ok = mbar_wait_bounded(s_full + 2 * s + (j & 1), (j >> 1) & 1, p.err_flag);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
+            const int buf = g % kBufs;
+            ok = tree_wait(s_full + kBufs * s + buf, (g / kBufs) & 1, p.err_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if ((flags & kLast) && (warp & 3) == 0 && lane == 0) load_queries(t + 1);
+            // the tokens of the tile that this row sees
+            uint32_t see[kWords];
+            if (!(flags & kPlain)) {
+                const TileMeta tile = meta[mt];
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    const int left = tile.valid - 32 * w;  // from this word on
+                    uint32_t bits = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0u;
+                    if (flags & kTree) {
+                        const int first = tile.start + 32 * w;  // the word's first node
+                        if (!live || left <= 0)
+                            bits = 0u;
+                        else if (p.masks)
+                            bits &= tile.start == 0 ? tree_bits[w]
+                                                    : (uint32_t)__ldg(p.masks + (int64_t)(tile.first + node) * p.words + (first >> 5));
+                        else
+                            bits &= node < first ? 0u : node - first >= 31 ? 0xffffffffu : (2u << (node - first)) - 1;
+                    } else if (flags >> kHoles) {
+                        for (int x = 0; x < 32; ++x)
+                            if ((flags >> (kHoles + (32 * w + x) / p.block_size)) & 1) bits &= ~(1u << x);
+                    }
+                    see[w] = bits;
+                    seen |= bits != 0;
+                }
+                // V rows past the end become zeros, whatever the ring held, and values that are not finite
+                // leave drafted rows that some rows do not see: before any weight of zero meets them.  (The
+                // scores of tile t are there, so V(t - 2), the last user of the slot or a later one, has
+                // been used up: the parity of `full` is that of V(t).)
+                if ((flags & kTree) || (s == 0 && tile.valid < kTileN)) {
+                    const int it = v_item(t);
+                    ok = tree_wait(full + it % kSlots, (it / kSlots) & 1, p.err_flag);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    const uint32_t v0 = smem_addr(ring) + it % kSlots * C::kTileBytes;
+                    const bool two = STREAMS == 2 && (flags & kTwo) && (flags & kTree);
+                    bool odd = false;
+#pragma unroll 4
+                    for (int x = two ? threadIdx.x : r; x < C::kTileBytes / 16; x += two ? 2 * kTileM : kTileM) {
+                        const uint32_t at = v0 + x * 16;
+                        if (((x >> 3) & (kTileN - 1)) >= tile.valid) {
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+                        } else if (flags & kTree) {
+                            const uint4 v = lds128(at);
+                            if (not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w)) {
+                                odd = true;
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(finite2(v.x)),
+                                             "r"(finite2(v.y)), "r"(finite2(v.z)), "r"(finite2(v.w))
+                                             : "memory");
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    // all rows of the unit learn of it, and all of the tile is clean before any of them goes on
+                    if (flags & kTree) dirty |= two ? softmax_any<2 * kTileM>(odd) : softmax_any<kTileM>(odd);
+                    __syncwarp();
+                }
+            } else {
+                seen = true;
             }
             __syncwarp();
             tc_fence_after();
-            const uint32_t s_addr = base + (j & 1) * kTileN;
+            const uint32_t s_addr = base + buf * kTileN;
             float x[kTileN];
-            tmem_ld32(s_addr, x);
-            tmem_ld32(s_addr + 32, x + 32);
+#pragma unroll
+            for (int q = 0; q < kTileN / 32; ++q) tmem_ld32(s_addr + 32 * q, x + 32 * q);
             tmem_wait_ld();
             if (flip) {
 #pragma unroll
                 for (int i = 0; i < kTileN; ++i) x[i] = -x[i];
             }
-            if (!__all_sync(0xffffffffu, (see[0] & see[1]) == 0xffffffffu)) {
+            if (!(flags & kPlain)) {
 #pragma unroll
-                for (int i = 0; i < kTileN; ++i)
-                    x[i] = (see[i >> 5] >> (i & 31)) & 1u ? x[i] : -INFINITY;
+                for (int i = 0; i < kTileN; ++i) x[i] = (see[i >> 5] >> (i & 31)) & 1u ? x[i] : -INFINITY;
             }
             float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
             for (int i = 4; i < kTileN; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
-            const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            if (__any_sync(0xffffffffu, mt > m + rise)) {
-                const float next = fmaxf(m, mt);
+            const float tile_max = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            if (__any_sync(0xffffffffu, tile_max > m + rise)) {
+                const float next = fmaxf(m, tile_max);
                 const float down = next == -INFINITY ? 1.f : fast_exp2((m - next) * c);
                 m = next;
                 l *= down;
-                if (j > 0) {  // O has been written: wait for the last product, then rescale it
-                    ok = mbar_wait_bounded(pv_done + s, (j - 1) & 1, p.err_flag);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                if (!(flags & kFirst)) {  // O has been written: wait for the last product, then rescale it
+                    ok = tree_wait(pv_done + s, (g - 1) & 1, p.err_flag);
+                    if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int q = 0; q < HEAD_DIM / 32; ++q) {
-                        float o[32];
-                        tmem_ld32(o_addr + 32 * q, o);
+                    for (int q = 0; q < HEAD_DIM / 16; ++q) {
+                        uint32_t w[16];
+                        tmem_ld16(o_addr + 16 * q, w);
                         tmem_wait_ld();
-                        uint32_t w[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * down);
-                        tmem_st32(o_addr + 32 * q, w);
+                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * down);
+                        tmem_st16(o_addr + 16 * q, w);
                     }
                 }
             }
             const float bias = m == -INFINITY ? 0.f : -m * c;
-            uint32_t w[kTileN / 2];
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 c2 = make_float2(c, c), bias2 = make_float2(bias, bias);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int i = 0; i < kTileN; i += 2) {
-                const float p0 = fast_exp2(fmaf(x[i], c, bias)), p1 = fast_exp2(fmaf(x[i + 1], c, bias));
-                sum[i & 2] += p0;
-                sum[(i & 2) + 1] += p1;
-                w[i / 2] = pack_bf16x2(p0, p1);
+            for (int q = 0; q < kTileN / 32; ++q) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 e = fma2(make_float2(x[32 * q + 2 * i], x[32 * q + 2 * i + 1]), c2, bias2);
+                    const float2 pr = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                    sum[i & 1] = add2(sum[i & 1], pr);
+                    w[i] = pack_bf16x2(pr.x, pr.y);
+                }
+                tmem_st16(s_addr + 16 * q, w);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st32(s_addr, w);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full + 2 * s + (j & 1));
-        }
-        // A barrier of its own: pv_done may be one or two phases ahead of this thread by now, and a
-        // parity tells only neighbouring phases apart.
-        if (ok) ok = mbar_wait_bounded(o_done + s, 0, p.err_flag);
-        if (__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) {
+                mbar_arrive(p_full + kBufs * s + buf);
+            }
+            ++g;
+            if (!(flags & kLast)) {
+                if (lane == 0) mbar_arrive(meta_free + mt);
+                continue;
+            }
+
+            // ---- the piece's output ----
+            const TileMeta tile = meta[mt];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(meta_free + mt);
+            ok = tree_wait(o_done + s, pieces++ & 1, p.err_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             // The state's two special cases: a NaN or +inf score (l is NaN) gets m = +inf, so that joining
-            // partitions keeps it; a row that saw only scores of -inf keeps m = -inf with l = NaN, so
-            // that a partition with a finite score outweighs it.  Nothing seen: m = -inf, l = 0.
+            // pieces keeps it; a row that saw only scores of -inf keeps m = -inf with l = NaN, so that a
+            // piece with a finite score outweighs it.  Nothing seen: m = -inf, l = 0.
             if (l != l)
                 m = INFINITY;
             else if (m == -INFINITY && seen)
                 l = NAN;
-            const int64_t row = (int64_t)(seq.first + node) * p.q_heads + h * G + r % G;
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            const bool whole = tile.dest < 0;
+            const int64_t state = (int64_t)tile.dest * (STREAMS * kTileM) + s * kTileM;  // of the stream's row 0
+            // Rows leave through shared memory: a lane holds a row, but four lanes store 64 bytes of one,
+            // eight rows at a time.  Chunk k of row w is at k ^ (w / 2 % 4): no bank conflicts either way.
+            const uint32_t mine = smem_addr(stage) + warp * 2048;
+            const int w0 = (warp & 3) * 32;  // the warp's first row of the stream
+            const int node_base = tile.place / p.kv_heads + s * tile_nodes;
+            auto store64 = [&](int col, const uint4 (&v)[4]) {
+                __syncwarp();
 #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)),
+                                 "r"(v[k].x), "r"(v[k].y), "r"(v[k].z), "r"(v[k].w)
+                                 : "memory");
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int w = 8 * k + (lane >> 2), row = w0 + w;
+                    const uint4 x = lds128(mine + w * 64 + (((lane & 3) ^ ((w >> 1) & 3)) << 4));
+                    const int n = node_base + (row >> p.group_shift);
+                    if (n >= tile.nodes) continue;
+                    char *dst = whole ? reinterpret_cast<char *>(p.out) +
+                                            (((int64_t)(tile.first + n) * p.q_heads + h * G + (row & (G - 1))) * HEAD_DIM + col) * 2
+                                      : reinterpret_cast<char *>(p.part_o) + ((state + row) * HEAD_DIM + col) * 4;
+                    *reinterpret_cast<uint4 *>(dst + (lane & 3) * 16) = x;
+                }
+            };
+#pragma unroll 1
             for (int q = 0; q < HEAD_DIM / 32; ++q) {
                 float o[32];
                 __syncwarp();
                 tmem_ld32(o_addr + 32 * q, o);
                 tmem_wait_ld();
                 if (live && dirty) {  // the values that were kept out of the product
-                    for (int k = 0; k < reach; ++k) {
-                        const bool sees = p.masks ? (__ldg(p.masks + (int64_t)(seq.first + node) * p.words + (k >> 5)) >> (k & 31)) & 1
+                    for (int k = 0; k < tile.nodes; ++k) {
+                        const bool sees = p.masks ? (__ldg(p.masks + (int64_t)(tile.first + node) * p.words + (k >> 5)) >> (k & 31)) & 1
                                                   : k <= node;
                         if (!sees) continue;
-                        const uint16_t *src = p.v_tree + (int64_t)(seq.first + k) * p.v_stride + h * HEAD_DIM + 32 * q;
+                        const uint16_t *src = p.v_tree + (int64_t)(tile.first + k) * p.v_stride + h * HEAD_DIM + 32 * q;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const uint32_t bits = (uint32_t)src[i] << 16;
@@ -595,21 +916,31 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
-                if (live && whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * HEAD_DIM + 32 * q);
+                uint4 v[4];
+                if (whole) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                            pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-                } else if (live) {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + (row * p.num_parts + part) * HEAD_DIM + 32 * q);
+                        v[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                    store64(32 * q, v);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = make_uint4(__float_as_uint(o[16 * half + 4 * i]), __float_as_uint(o[16 * half + 4 * i + 1]),
+                                              __float_as_uint(o[16 * half + 4 * i + 2]), __float_as_uint(o[16 * half + 4 * i + 3]));
+                        store64(32 * q + 16 * half, v);
+                    }
                 }
             }
             if (live && !whole)
-                *reinterpret_cast<float2 *>(p.part_ml + (row * p.num_parts + part) * 2) = make_float2(m == -INFINITY ? m : m * c, l);
+                *reinterpret_cast<float2 *>(p.part_ml + (state + r) * 2) = make_float2(m == -INFINITY ? m : m * c, l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free + s);
         }
+        if (q_loads > 0) mbar_wait_bounded(q_full + s, (q_loads - 1) & 1, p.err_flag);  // the last copy has landed
     }
 
     __syncwarp();
@@ -621,52 +952,117 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
     }
 }
 
-// Joins the partitions of one (row, query head), one to a warp:
+// Joins the states of the units that were cut:
 //   out = sum_p 2^(m_p - M) l_p o_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p.
-constexpr int kTreeReduceWarps = 8;
+// CTA (i, y): if cut i + 1 is the first one inside its unit, rows [32 y, 32 y + 32) of that unit.  The
+// piece before the first cut is CTA i's second state, the pieces after the cuts are the first states of
+// the CTAs that begin there.  Which cuts those are follows from the lengths, so all of it is worked out
+// while the attention still runs; four rows of a warp are in flight at once.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 32;
 
-template <int HEAD_DIM>
-__global__ void __launch_bounds__(kTreeReduceWarps * 32) tree_reduce_kernel(const TreeParams p) {
-    constexpr int V = HEAD_DIM / 32;
-    const int lane = threadIdx.x & 31;
-    const int item = blockIdx.x * kTreeReduceWarps + (threadIdx.x >> 5);
-    const TreeSeq seq = tree_seq(p, blockIdx.y);
-    const int parts = (seq.len + p.part_tokens - 1) / p.part_tokens;
-    if (parts <= 1 || item >= seq.nodes * p.q_heads) return;  // written by the attention itself
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t row = (int64_t)seq.first * p.q_heads + item;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + row * p.num_parts;
-    const float *po = p.part_o + row * p.num_parts * HEAD_DIM + lane * V;
-    float M = -INFINITY, none = 0.f;
-    for (int i = lane; i < parts; i += 32) {
-        const float2 s = ml[i];
-        M = fmaxf(M, s.x);
-        none += s.x == -INFINITY ? s.y : 0.f;  // NaN where all scores of a partition were -inf
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) {
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        none += __shfl_xor_sync(0xffffffffu, none, off);
-    }
-    float acc[V], den = 0.f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const float2 s = ml[i];
-            const float w = s.x == -INFINITY ? 0.f : fast_exp2(s.x - M) * s.y;
-            if (s.x != -INFINITY) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] += w * po[(int64_t)i * HEAD_DIM + e];
+template <int HEAD_DIM, int STREAMS>
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams p) {
+    using C = TreeCfg<HEAD_DIM, STREAMS>;
+    constexpr int V = HEAD_DIM / 32, R = kJoinRows / kJoinWarps;
+    constexpr int kRows = STREAMS * kTileM;
+    __shared__ int64_t scan[32];
+    __shared__ TreeMark s_at;
+    __shared__ int s_pieces;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = blockIdx.x + 1, ctas = gridDim.x + 1;
+    if (threadIdx.x == 0) s_pieces = 0;
+    const TreeLine n = tree_line<HEAD_DIM, STREAMS, kJoinWarps * 32>(p, ctas, scan, false);
+    int64_t at = tree_cut(n, first) - n.before;
+    if (at >= 0 && at < n.mine && first < n.count) {  // this thread's sequences hold the cut
+        int64_t begin = n.before;
+        for (int b = n.b0; b < n.b1; ++b) {
+            const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, tree_seq(p, b));
+            const int weight = u.tiles + C::kUnitCost;
+            const int64_t all = (int64_t)(u.chunks * p.kv_heads) * weight;
+            if (at >= all) {
+                at -= all;
+                begin += all;
+                continue;
             }
-            den += w;
+            const TreeMark m = tree_mark<HEAD_DIM, STREAMS>(p, u, b, at);
+            auto inside = [&](int i) {  // cut i is one of this unit
+                if (i >= n.count) return false;
+                const int64_t x = tree_cut(n, i) - begin;
+                if (x < (int64_t)m.unit * weight || x >= (int64_t)(m.unit + 1) * weight) return false;
+                const TreeMark y = tree_mark<HEAD_DIM, STREAMS>(p, u, b, x);
+                return y.unit == m.unit && y.tile != 0;
+            };
+            if (m.tile != 0 && !inside(first - 1)) {
+                int pieces = 2;
+                while (inside(first + pieces - 1)) ++pieces;
+                s_at = m;
+                s_pieces = pieces;
+            }
+            break;
         }
     }
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + row * HEAD_DIM + lane * V);
+    __syncthreads();
+    const int pieces = s_pieces;
+    if (pieces == 0) return;
+    const TreeSeq seq = tree_seq(p, s_at.b);
+    const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, seq);
+    const int h = s_at.unit / u.chunks;
+    const int node0 = (s_at.unit - h * u.chunks) * (STREAMS * kTileM >> p.group_shift);
+    const int r0 = blockIdx.y * kJoinRows + warp * R;
+    if (node0 + (r0 >> p.group_shift) >= seq.nodes) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // state of piece k: 2 * first - 1, then 2 * first, 2 * first + 2, ...
+    auto state = [&](int k) { return (int64_t)(k == 0 ? 2 * first - 1 : 2 * (first + k - 1)) * kRows + r0; };
+    float M[R], den[R], none[R], acc[R][V];
 #pragma unroll
-    for (int e = 0; e < V; e += 2)
-        dst[e / 2] = M == -INFINITY ? pack_bf16x2(none, none) : pack_bf16x2(acc[e] / den, acc[e + 1] / den);
+    for (int r = 0; r < R; ++r) {
+        M[r] = -INFINITY;
+        den[r] = none[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[r][e] = 0.f;
+    }
+#pragma unroll 2
+    for (int k = 0; k < pieces; ++k) {
+        float2 ml[R];
+        float o[R][V];
+        // rows past the last node hold whatever the workspace held: they are not stored below
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            ml[r] = *(reinterpret_cast<const float2 *>(p.part_ml) + state(k) + r);
+            const float *src = p.part_o + (state(k) + r) * HEAD_DIM + lane * V;
+            if constexpr (V == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(src);
+                o[r][0] = v.x, o[r][1] = v.y, o[r][2] = v.z, o[r][3] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(src);
+                o[r][0] = v.x, o[r][1] = v.y;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (ml[r].x == -INFINITY) {  // nothing, or (NaN) only scores of -inf
+                none[r] += ml[r].y;
+                continue;
+            }
+            const float top = fmaxf(M[r], ml[r].x);
+            const float down = fast_exp2(M[r] - top), w = fast_exp2(ml[r].x - top) * ml[r].y;
+            M[r] = top;
+            den[r] = den[r] * down + w;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[r][e] = acc[r][e] * down + w * o[r][e];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = r0 + r, node = node0 + (row >> p.group_shift);
+        if (node >= seq.nodes) break;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(
+            p.out + ((int64_t)(seq.first + node) * p.q_heads + h * p.group + (row & (p.group - 1))) * HEAD_DIM + lane * V);
+#pragma unroll
+        for (int e = 0; e < V; e += 2)
+            dst[e / 2] = M[r] == -INFINITY ? pack_bf16x2(none[r], none[r]) : pack_bf16x2(acc[r][e] / den[r], acc[r][e + 1] / den[r]);
+    }
 }
 
 }  // namespace

@@ -42,6 +42,7 @@ def test_decode_tree_refusals():
         assert call(**bad) == INVALID, bad
     for bad in (dict(d=96), dict(bs=12), dict(Hq=6, Hkv=4), dict(Hq=32, Hkv=2), dict(NB=1 << 30), dict(B=70000)):
         assert call(**bad) == UNSUPPORTED, bad
+    assert call(pt=128, maxlen=257) == INVALID  # needs a workspace
     assert call(pt=64) == INVALID and call(pt=16) == INVALID  # partitions are multiples of 128 tokens
 
 
@@ -157,4 +158,6 @@ def test_tree_workspace_size_of_unsplit_calls():
     assert pa.pa_decode_tree_workspace_size(4, 32, 8, 2, 128, 16, 4096, 8, -1) == 0
     assert pa.pa_decode_tree_workspace_size(0, 0, 8, 2, 128, 16, 4096, 8, 0) == 0
     assert pa.pa_decode_tree_workspace_size(4, 32, 8, 2, 128, 16, 0, 8, 0) == 0
-    assert pa.pa_decode_tree_partition_tokens(4, 8, 2, 128, 16, 4096, 8, -1) == -1
+    assert pa.pa_decode_tree_workspace_size(4, 32, 8, 2, 128, 16, 512, 8, 0) == 0  # a few tiles: never cut
+    assert pa.pa_decode_tree_workspace_size(4, 32, 8, 2, 128, 16, 256, 8, 128) == 0
+    assert pa.pa_decode_tree_workspace_size(4, 32, 8, 2, 128, 16, 4096, 8, 0) > 0
