@@ -201,8 +201,8 @@ int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tre
         return PA_ERR_UNSUPPORTED;
     pa::TreeMaps m;
     if (!pa::tree_rows_map(&m.q, q, q_stride, num_rows, num_q_heads, head_dim, p.group, pa::kTileM / p.group) ||
-        !pa::tree_rows_map(&m.kt, k_tree, k_stride, num_rows, num_kv_heads, head_dim, 1, tile) ||
-        !pa::tree_rows_map(&m.vt, v_tree, v_stride, num_rows, num_kv_heads, head_dim, 1, tile) ||
+        !pa::tree_rows_map(&m.kt, k_tree, k_stride, num_rows, num_kv_heads, head_dim, 1, pa::kTreeBox) ||
+        !pa::tree_rows_map(&m.vt, v_tree, v_stride, num_rows, num_kv_heads, head_dim, 1, pa::kTreeBox) ||
         !pa::tree_pool_map(&m.k, k_cache, rows, head_dim, block_size) ||
         !pa::tree_pool_map(&m.v, v_cache, rows, head_dim, block_size))
         return PA_ERR_CUDA;

@@ -48,6 +48,7 @@ namespace {
 
 constexpr float kTreeLog2e = 1.4426950408889634f;
 constexpr int kTileM = 128;        // query rows of one stream
+constexpr int kTreeBox = 16;        // drafted rows of one TMA box
 constexpr float kMaxRise = 8.0f;   // log2 of the largest weight before the reference moves
 
 template <int HEAD_DIM, int STREAMS>
@@ -63,15 +64,15 @@ struct TreeCfg {
     static constexpr int kMetas = 16;                          // tile descriptions
     static constexpr int kCtasPerSm = STREAMS == 1 ? 2 : 1;
     static constexpr int kSoftmaxWarps = 4 * STREAMS;
-    static constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+    static constexpr int kThreads = (kSoftmaxWarps + 1 + STREAMS) * 32;  // + producer, product warps
     // TMEM of one stream: the score buffers (P in the first half of each), then O.
     static constexpr int kStreamCols = 128 + 128;
     static constexpr int kCols = STREAMS * kStreamCols;
-    static constexpr int kBars = 2 * kSlots + 2 * kMetas + STREAMS * (2 * kBufs + 4) + 1;
+    static constexpr int kBars = 2 * kSlots + 2 * kMetas + STREAMS * (2 * kBufs + 5);
     static constexpr int kDataBytes = STREAMS * kQBytes + kSlots * kTileBytes;
     // Each softmax warp turns its rows of the output into whole 64-byte pieces here.
     static constexpr int kStageBytes = kSoftmaxWarps * 2048;
-    static constexpr int kTailBytes = kStageBytes + kMetas * 32 + kBars * 8 + 32 * 8 + 2 * 16 + 16;
+    static constexpr int kTailBytes = kStageBytes + kMetas * 48 + kBars * 8 + 32 * 8 + 2 * 16 + 16;
     static constexpr int kSmemBytes = 1024 /* align slack */ + kDataBytes + kTailBytes;
     static_assert(kCtasPerSm * kCols <= 512, "TMEM columns of an SM");
     static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
@@ -180,6 +181,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
         : "memory");
+}
+
+// The lowest n bits (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    uint32_t x;
+    asm("shl.b32 %0, %1, %2;" : "=r"(x) : "r"(0xffffffffu), "r"((uint32_t)max(n, 0)));  // a shift by 32 or more gives 0
+    return ~x;
 }
 
 // Two fp32 operations in one instruction.
@@ -361,15 +369,15 @@ __device__ __forceinline__ void tree_marks(const TreeParams &p, int ctas, int i,
 }
 
 // One tile, as the producer describes it to the other warps.
-enum { kFirst = 1, kLast = 2, kTree = 4, kTwo = 8, kEnd = 16, kPlain = 32, kHoles = 8 /* shift of 16 page bits */ };
+enum { kFirst = 1, kLast = 2, kTree = 4, kTwo = 8, kEnd = 16, kPlain = 32 };
 struct __align__(16) TileMeta {
-    int flags;   // first / last of its piece, drafted rows, both streams have rows, no tile, seen by all rows
-                 // as a whole; pages with a bad block
-    int valid;   // tokens (or nodes) in it
+    int flags;   // first / last of its piece, drafted rows, both streams have rows, no tile, seen whole by all
+                 // rows
     int start;   // first token (or node)
+    int valid;   // tokens (or nodes) in it
     int dest;    // -1: the piece is a whole unit; else its partial state's place
-    int b, first, nodes;
-    int place;   // node0 * kv_heads + kv head
+    int first, nodes, node0, h;
+    uint32_t words[4];  // the tokens that are there: not past the end, not in a bad block
 };
 
 template <int HEAD_DIM, int STREAMS>
@@ -388,7 +396,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
     TreeMark *mark = reinterpret_cast<TreeMark *>(meta + C::kMetas);  // [2]
     int64_t *scan = reinterpret_cast<int64_t *>(mark + 2);            // [32]
     uint64_t *full = reinterpret_cast<uint64_t *>(scan + 32);
-    uint64_t *empty = full + kSlots;
+    uint64_t *empty = full + kSlots;              // every stream has used the tile
     uint64_t *meta_full = empty + kSlots;
     uint64_t *meta_free = meta_full + C::kMetas;  // every softmax warp is done with the description
     uint64_t *s_full = meta_free + C::kMetas;     // [stream][buffer]: scores are in TMEM
@@ -397,33 +405,29 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
     uint64_t *pv_done = q_full + STREAMS;         // [stream]: a tile has been added to O
     uint64_t *o_done = pv_done + STREAMS;         // [stream]: a piece's last tile has
     uint64_t *o_free = o_done + STREAMS;          // [stream]: a piece's O has been read
-    uint64_t *drained = o_free + STREAMS;         // every product has completed
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
+    uint64_t *drained = o_free + STREAMS;         // [stream]: every product has completed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + STREAMS);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group;
     const int tile_nodes = kTileM / G;  // nodes of one stream's rows
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(full + s, 1);
-            mbar_init(empty + s, 1);
-        }
-        for (int s = 0; s < C::kMetas; ++s) {
-            mbar_init(meta_full + s, 1);
-            mbar_init(meta_free + s, C::kSoftmaxWarps);
-        }
-        for (int s = 0; s < kBufs * STREAMS; ++s) {
-            mbar_init(s_full + s, 1);
-            mbar_init(p_full + s, 4);
-        }
-        for (int s = 0; s < STREAMS; ++s) {
-            mbar_init(q_full + s, 1);
-            mbar_init(pv_done + s, 1);
-            mbar_init(o_done + s, 1);
-            mbar_init(o_free + s, 4);
-        }
-        mbar_init(drained, 1);
+    if (warp == C::kSoftmaxWarps && lane == 0) {
+        prefetch_tensormap(&k_map);
+        prefetch_tensormap(&v_map);
+        prefetch_tensormap(&q_map);
+        prefetch_tensormap(&kt_map);
+        prefetch_tensormap(&vt_map);
+    }
+    // One barrier for each thread: all are in one row, their counts follow from where they are.
+    static_assert(C::kBars <= C::kThreads, "one thread initialises one barrier");
+    if (threadIdx.x < C::kBars) {
+        uint64_t *bar = full + threadIdx.x;
+        mbar_init(bar, bar >= empty && bar < meta_full       ? STREAMS
+                       : bar >= meta_free && bar < s_full    ? C::kSoftmaxWarps
+                       : bar >= p_full && bar < q_full       ? 4
+                       : bar >= o_free && bar < drained      ? 4
+                                                             : 1);
         fence_mbar_init();
     }
     if (warp == C::kSoftmaxWarps + 1) {
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         struct Tile {
             int flags, start, valid, id;
             bool mine;
-            int dest, b, first, nodes, place, h;  // the piece's
+            int dest, first, nodes, node0, h;  // the piece's
         };
         Tile piece{};
         int stop = 0;       // the piece's tiles end here
@@ -486,14 +490,12 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                     if (cur.b + 1 < p.batch) ahead = tree_seq(p, cur.b + 1);
                 }
                 piece.h = of.chunks == 1 ? cur.unit : cur.unit / of.chunks;
-                const int node0 = (cur.unit - piece.h * of.chunks) * (STREAMS * tile_nodes);
-                piece.place = node0 * p.kv_heads + piece.h;
+                piece.node0 = (cur.unit - piece.h * of.chunks) * (STREAMS * tile_nodes);
                 stop = cur.b == end.b && cur.unit == end.unit ? end.tile : of.tiles;
                 piece.dest = cur.tile == 0 && stop == of.tiles ? -1 : 2 * (int)blockIdx.x + (cur.tile == 0);
-                piece.b = cur.b;
                 piece.first = seq.first;
                 piece.nodes = seq.nodes;
-                piece.flags = kFirst | (STREAMS == 2 && node0 + tile_nodes < seq.nodes ? kTwo : 0);
+                piece.flags = kFirst | (STREAMS == 2 && piece.node0 + tile_nodes < seq.nodes ? kTwo : 0);
                 entries = p.tables + (int64_t)cur.b * p.max_blocks + page;
             }
             Tile t = piece;
@@ -529,22 +531,27 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             const int slot = it % kSlots;
             uint8_t *dst = ring + slot * C::kTileBytes;
             if (lane == slot) landed = it;
+            // V past the end is read from outside of the tensor, which gives zeros: whatever the ring held
+            // must not meet a weight of zero.  (The rest of a partly used box is zeroed by the softmax warps.)
             if (t.flags & kTree) {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(full + slot, C::kTileBytes);
-                    for (int x = 0; x < C::kBoxes; ++x)
-                        tma_load_3d(dst + x * C::kBoxBytes, is_k ? &kt_map : &vt_map, x * 64, t.h, t.first + t.start,
-                                    full + slot);
-                }
+                if (lane == 0)
+                    mbar_arrive_expect_tx(full + slot, is_k ? C::kBoxes * ((t.valid + kTreeBox - 1) / kTreeBox) * kTreeBox * 128
+                                                            : C::kTileBytes);
+                __syncwarp();
+                const int box_row = page * kTreeBox;
+                if (box_row < (is_k ? t.valid : kTileN))
+                    tma_load_3d(dst + box * C::kBoxBytes + box_row * 128, is_k ? &kt_map : &vt_map, box * 64, t.h,
+                                box_row < t.valid ? t.first + t.start + box_row : p.num_rows, full + slot);
                 return;
             }
-            const int loads = __popc(__ballot_sync(0xffffffffu, t.mine));
+            const bool mine = t.mine || (!is_k && page < pages);
+            const int loads = __popc(__ballot_sync(0xffffffffu, mine));
             if (lane == 0) mbar_arrive_expect_tx(full + slot, loads * p.block_size * 128);
             __syncwarp();
-            if (t.mine) {
-                // a bad block reads as zeros (a row outside of the map)
-                const bool bad = t.id < 0 || t.id >= p.num_blocks;
-                const int row = bad ? p.pool_rows : (int)(((int64_t)t.id * p.kv_heads + t.h) * p.block_size);
+            if (mine) {
+                // a bad block reads as zeros too
+                const bool none = !t.mine || t.id < 0 || t.id >= p.num_blocks;
+                const int row = none ? p.pool_rows : (int)(((int64_t)t.id * p.kv_heads + t.h) * p.block_size);
                 tma_load_2d(dst + box * C::kBoxBytes + page * p.block_size * 128, is_k ? &k_map : &v_map, box * 64, row,
                             full + slot, policy);
             }
@@ -558,17 +565,33 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 const uint32_t holes = __ballot_sync(0xffffffffu, t0.mine && box == 0 && (t0.id < 0 || t0.id >= p.num_blocks));
                 if (holes) {
                     if (lane == 0) raise_flag(p.err_flag, PA_FLAG_BAD_BLOCK);
-                    for (int x = 0; x < pages; ++x)
-                        if ((holes >> (x * C::kBoxes)) & 1) t0.flags |= 1 << (kHoles + x);
                     t0.flags &= ~kPlain;
                 }
                 const int mt = t % C::kMetas;
                 const bool free = t < C::kMetas || tree_wait(meta_free + mt, (t / C::kMetas - 1) & 1, p.err_flag);
                 if (!__all_sync(0xffffffffu, free)) break;
                 if (lane == 0) {
-                    meta[mt] = TileMeta{t0.flags, t0.valid, t0.start, t0.dest, t0.b, t0.first, t0.nodes, t0.place};
-                    mbar_arrive(meta_full + mt);
+                    TileMeta &d = meta[mt];
+                    d.flags = t0.flags;
+                    d.start = t0.start;
+                    d.valid = t0.valid;
+                    d.dest = t0.dest;
+                    d.first = t0.first;
+                    d.nodes = t0.nodes;
+                    d.node0 = t0.node0;
+                    d.h = t0.h;
                 }
+                if (!(t0.flags & (kPlain | kEnd)) && lane < 4) {
+                    uint32_t bits = low_bits(t0.valid - 32 * lane);
+                    if (holes)
+                        for (int x = 0; x < 32; ++x) {
+                            const int at = (32 * lane + x) / p.block_size;
+                            if (at < pages && ((holes >> (at * C::kBoxes)) & 1)) bits &= ~(1u << x);
+                        }
+                    meta[mt].words[lane] = bits;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(meta_full + mt);
                 if (t0.flags & kEnd)
                     n = t;
                 else
@@ -586,85 +609,79 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         }
         // Every copy has landed before the CTA ends (it has, unless a wait ran out).
         if (lane < kSlots && landed >= 0) mbar_wait_bounded(full + lane, (landed / kSlots) & 1, p.err_flag);
-    } else if (warp == C::kSoftmaxWarps + 1) {
-        // ---------------- products, issued by one thread ----------------
+    } else if (warp > C::kSoftmaxWarps) {
+        // ---------------- products, issued by one thread for each stream ----------------
+        // O += P V of tile t - kBufs, then S = Q K^T of tile t.
         if (lane == 0) {
             constexpr uint32_t kQkDesc = tree_idesc(kTileN, false), kPvDesc = tree_idesc(HEAD_DIM, true);
+            const int s = warp - (C::kSoftmaxWarps + 1);
             // Descriptors of the queries and of ring slot 0; a step through the operand or to another
             // slot adds to the start address (16-byte units), which never carries out of its field.
-            const uint64_t q_desc = umma_desc_k_sw128(smem_addr(smem));
+            const uint64_t q_desc = umma_desc_k_sw128(smem_addr(smem + s * C::kQBytes));
             const uint64_t k_desc = umma_desc_k_sw128(smem_addr(ring));
             const uint64_t v_desc = umma_desc_mn_sw128(smem_addr(ring), C::kBoxBytes);
-            // per stream: tiles whose scores / products were issued, and their pieces
-            int scored[STREAMS] = {}, added[STREAMS] = {}, pieces_q[STREAMS] = {}, pieces_o[STREAMS] = {};
-            int queue[kBufs] = {};  // flags of the tiles between the two
+            const uint32_t base = tmem + s * C::kStreamCols;
+            int scored = 0, added = 0;      // tiles whose scores / products were issued
+            int pieces_q = 0, pieces_o = 0;
+            int queue[kBufs] = {};          // flags of the tiles between the two
             auto wait_item = [&](int it) { return tree_wait(full + it % kSlots, (it / kSlots) & 1, p.err_flag); };
             bool ok = true, over = false;
             for (int t = 0; ok; ++t) {
-                // O += P V of tile t - kBufs, then S = Q K^T of tile t, one stream after the other: while
-                // one waits for its softmax, the other has the tensor cores
-                const int f_pv = t >= kBufs ? queue[0] : 0;
-                const bool pv = t >= kBufs && !(f_pv & kEnd);
-                if (t >= kBufs && !pv) break;
-                int f_qk = kEnd;
-                uint64_t vd = 0, kd = 0;
-                if (pv) {
-                    if (!(ok = wait_item(v_item(t - kBufs)))) break;
-                    vd = v_desc + (uint32_t)(v_item(t - kBufs) % kSlots * (C::kTileBytes / 16));
-                }
-#pragma unroll
-                for (int s = 0; s < STREAMS; ++s) {
-                    if (ok && pv && (s == 0 || (f_pv & kTwo))) {
-                        const int g = added[s]++;
-                        ok = tree_wait(p_full + kBufs * s + g % kBufs, (g / kBufs) & 1, p.err_flag);
+                if (t >= kBufs) {
+                    const int f = queue[0], it = v_item(t - kBufs);
+                    if (f & kEnd) break;
+                    if (!(ok = wait_item(it))) break;
+                    if (s == 0 || (f & kTwo)) {
+                        const int g = added++;
+                        if (!(ok = tree_wait(p_full + kBufs * s + g % kBufs, (g / kBufs) & 1, p.err_flag))) break;
                         // a new piece overwrites O: the last one's has to have been read
-                        if (ok && (f_pv & kFirst) && pieces_o[s]++ > 0) ok = tree_wait(o_free + s, pieces_o[s] & 1, p.err_flag);
-                        if (ok) {
-                            tc_fence_after();
-                            const uint32_t base = tmem + s * C::kStreamCols;
-                            const uint32_t a = base + g % kBufs * kTileN;
+                        if ((f & kFirst) && pieces_o++ > 0 && !(ok = tree_wait(o_free + s, pieces_o & 1, p.err_flag))) break;
+                        tc_fence_after();
+                        const uint64_t vd = v_desc + (uint32_t)(it % kSlots * (C::kTileBytes / 16));
+                        const uint32_t a = base + g % kBufs * kTileN;
 #pragma unroll
-                            for (int i = 0; i < kTileN / 16; ++i)
-                                umma_bf16_ts(base + 128, a + 8 * i, vd + i * (2048 / 16), kPvDesc, !(f_pv & kFirst) || i > 0);
-                            umma_commit(pv_done + s);
-                            if (f_pv & kLast) umma_commit(o_done + s);
-                        }
-                    }
-                    if (s == 0 && ok && !over) {
-                        ok = tree_wait(meta_full + t % C::kMetas, (t / C::kMetas) & 1, p.err_flag);
-                        if (ok) f_qk = *const_cast<volatile int *>(&meta[t % C::kMetas].flags);
-                        over = f_qk & kEnd;
-                        if (ok && !over) {
-                            ok = wait_item(k_item(t));
-                            kd = k_desc + (uint32_t)(k_item(t) % kSlots * (C::kTileBytes / 16));
-                        }
-                    }
-                    if (ok && !over && (s == 0 || (f_qk & kTwo))) {
-                        if (f_qk & kFirst) ok = tree_wait(q_full + s, pieces_q[s]++ & 1, p.err_flag);
-                        const int g = scored[s]++;
-                        // the new scores take the place of an earlier tile's P: its product has to be done
-                        if (ok && g >= kBufs) ok = tree_wait(pv_done + s, (g - kBufs) & 1, p.err_flag);
-                        if (ok) {
-                            tc_fence_after();
-                            const uint64_t qd = q_desc + (uint32_t)(s * (C::kQBytes / 16));
-                            const uint32_t d = tmem + s * C::kStreamCols + g % kBufs * kTileN;
-#pragma unroll
-                            for (int i = 0; i < HEAD_DIM / 16; ++i)
-                                umma_bf16_ss(d, qd + ((i >> 2) * C::kQBoxBytes + (i & 3) * 32) / 16,
-                                             kd + ((i >> 2) * C::kBoxBytes + (i & 3) * 32) / 16, kQkDesc, i > 0);
-                            umma_commit(s_full + kBufs * s + g % kBufs);
-                        }
+                        for (int i = 0; i < kTileN / 16; ++i)
+                            umma_bf16_ts(base + 128, a + 8 * i, vd + i * (2048 / 16), kPvDesc, !(f & kFirst) || i > 0);
+                        umma_commit(pv_done + s);
+                        if (f & kLast) umma_commit(o_done + s);
+                        umma_commit(empty + it % kSlots);
+                    } else {
+                        mbar_arrive(empty + it % kSlots);
                     }
                 }
-                if (!ok) break;
-                if (pv) umma_commit(empty + v_item(t - kBufs) % kSlots);
-                if (!over) umma_commit(empty + k_item(t) % kSlots);
+                int f = kEnd;
+                if (!over) {
+                    if (!(ok = tree_wait(meta_full + t % C::kMetas, (t / C::kMetas) & 1, p.err_flag))) break;
+                    f = *const_cast<volatile int *>(&meta[t % C::kMetas].flags);
+                    over = f & kEnd;
+                }
+                if (!over) {
+                    const int it = k_item(t);
+                    if (!(ok = wait_item(it))) break;
+                    if (s == 0 || (f & kTwo)) {
+                        if ((f & kFirst) && !(ok = tree_wait(q_full + s, pieces_q++ & 1, p.err_flag))) break;
+                        const int g = scored++;
+                        // the new scores take the place of an earlier tile's P: its product has to be done
+                        if (g >= kBufs && !(ok = tree_wait(pv_done + s, (g - kBufs) & 1, p.err_flag))) break;
+                        tc_fence_after();
+                        const uint64_t kd = k_desc + (uint32_t)(it % kSlots * (C::kTileBytes / 16));
+                        const uint32_t d = base + g % kBufs * kTileN;
+#pragma unroll
+                        for (int i = 0; i < HEAD_DIM / 16; ++i)
+                            umma_bf16_ss(d, q_desc + ((i >> 2) * C::kQBoxBytes + (i & 3) * 32) / 16,
+                                         kd + ((i >> 2) * C::kBoxBytes + (i & 3) * 32) / 16, kQkDesc, i > 0);
+                        umma_commit(s_full + kBufs * s + g % kBufs);
+                        umma_commit(empty + it % kSlots);
+                    } else {
+                        mbar_arrive(empty + it % kSlots);
+                    }
+                }
 #pragma unroll
                 for (int x = 0; x + 1 < kBufs; ++x) queue[x] = queue[x + 1];
-                queue[kBufs - 1] = f_qk;
+                queue[kBufs - 1] = f;
             }
-            umma_commit(drained);
-            mbar_wait_bounded(drained, 0, p.err_flag);
+            umma_commit(drained + s);
+            mbar_wait_bounded(drained + s, 0, p.err_flag);
         }
     } else {
         // ---------------- softmax: one row to a thread ----------------
@@ -683,18 +700,18 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         auto load_queries = [&](int t) {
             if (!tree_wait(meta_full + t % C::kMetas, (t / C::kMetas) & 1, p.err_flag)) return;
             const volatile TileMeta &m = meta[t % C::kMetas];
-            const int f = m.flags, place = m.place, first = m.first;
+            const int f = m.flags, row = m.first + m.node0 + s * tile_nodes, head = m.h * G;
             if ((f & kEnd) || (s == 1 && !(f & kTwo))) return;
             mbar_arrive_expect_tx(q_full + s, C::kQBytes);
             for (int x = 0; x < C::kBoxes; ++x)
-                tma_load_3d(smem + s * C::kQBytes + x * C::kQBoxBytes, &q_map, x * 64, place % p.kv_heads * G,
-                            first + place / p.kv_heads + s * tile_nodes, q_full + s);
+                tma_load_3d(smem + s * C::kQBytes + x * C::kQBoxBytes, &q_map, x * 64, head, row, q_full + s);
             ++q_loads;
         };
         if ((warp & 3) == 0 && lane == 0) load_queries(0);
 
         constexpr int kWords = kTileN / 32;
-        int node = 0, h = 0, g = 0, pieces = 0;  // g: tiles of this stream so far
+        int g = 0, pieces = 0;  // tiles and pieces of this stream so far
+        int node = 0;           // of this thread's row
         bool live = false, seen = false, dirty = false;
         uint32_t tree_bits[kWords] = {};  // the row's mask of the first drafted tile
         float m = -INFINITY, l = 0.f;
@@ -712,17 +729,19 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 continue;
             }
             if (flags & kFirst) {
-                h = meta[mt].place % p.kv_heads;
-                node = meta[mt].place / p.kv_heads + s * tile_nodes + (r >> p.group_shift);
-                live = node < meta[mt].nodes;
+                const TileMeta &tile = meta[mt];
+                node = tile.node0 + s * tile_nodes + (r >> p.group_shift);
+                live = node < tile.nodes;
                 seen = dirty = false;
                 m = -INFINITY;
                 l = 0.f;
-                if (p.masks && live) {  // needed at the end of the piece: fetched now
+                // the nodes of the first drafted tile that the row sees: needed at the end of the piece, fetched now
 #pragma unroll
-                    for (int w = 0; w < kWords; ++w)
-                        tree_bits[w] = w < p.words ? (uint32_t)__ldg(p.masks + (int64_t)(meta[mt].first + node) * p.words + w) : 0u;
-                }
+                for (int w = 0; w < kWords; ++w)
+                    tree_bits[w] = !live ? 0u
+                                   : !p.masks ? low_bits(node + 1 - 32 * w)
+                                   : w < p.words ? (uint32_t)__ldg(p.masks + (int64_t)(tile.first + node) * p.words + w)
+                                                 : 0u;
             }
             const int buf = g % kBufs;
             ok = tree_wait(s_full + kBufs * s + buf, (g / kBufs) & 1, p.err_flag);
@@ -731,57 +750,21 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             // the tokens of the tile that this row sees
             uint32_t see[kWords];
             if (!(flags & kPlain)) {
-                const TileMeta tile = meta[mt];
+                const TileMeta &tile = meta[mt];
+                if ((flags & kTree) && tile.start > 0) {  // a later tile of a large tree
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) {
+                        const int word = tile.start / 32 + w;
+                        tree_bits[w] = !live ? 0u
+                                       : !p.masks ? low_bits(node + 1 - 32 * word)
+                                       : word < p.words ? (uint32_t)__ldg(p.masks + (int64_t)(tile.first + node) * p.words + word)
+                                                        : 0u;
+                    }
+                }
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) {
-                    const int left = tile.valid - 32 * w;  // from this word on
-                    uint32_t bits = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0u;
-                    if (flags & kTree) {
-                        const int first = tile.start + 32 * w;  // the word's first node
-                        if (!live || left <= 0)
-                            bits = 0u;
-                        else if (p.masks)
-                            bits &= tile.start == 0 ? tree_bits[w]
-                                                    : (uint32_t)__ldg(p.masks + (int64_t)(tile.first + node) * p.words + (first >> 5));
-                        else
-                            bits &= node < first ? 0u : node - first >= 31 ? 0xffffffffu : (2u << (node - first)) - 1;
-                    } else if (flags >> kHoles) {
-                        for (int x = 0; x < 32; ++x)
-                            if ((flags >> (kHoles + (32 * w + x) / p.block_size)) & 1) bits &= ~(1u << x);
-                    }
-                    see[w] = bits;
-                    seen |= bits != 0;
-                }
-                // V rows past the end become zeros, whatever the ring held, and values that are not finite
-                // leave drafted rows that some rows do not see: before any weight of zero meets them.  (The
-                // scores of tile t are there, so V(t - 2), the last user of the slot or a later one, has
-                // been used up: the parity of `full` is that of V(t).)
-                if ((flags & kTree) || (s == 0 && tile.valid < kTileN)) {
-                    const int it = v_item(t);
-                    ok = tree_wait(full + it % kSlots, (it / kSlots) & 1, p.err_flag);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    const uint32_t v0 = smem_addr(ring) + it % kSlots * C::kTileBytes;
-                    const bool two = STREAMS == 2 && (flags & kTwo) && (flags & kTree);
-                    bool odd = false;
-#pragma unroll 4
-                    for (int x = two ? threadIdx.x : r; x < C::kTileBytes / 16; x += two ? 2 * kTileM : kTileM) {
-                        const uint32_t at = v0 + x * 16;
-                        if (((x >> 3) & (kTileN - 1)) >= tile.valid) {
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
-                        } else if (flags & kTree) {
-                            const uint4 v = lds128(at);
-                            if (not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w)) {
-                                odd = true;
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(finite2(v.x)),
-                                             "r"(finite2(v.y)), "r"(finite2(v.z)), "r"(finite2(v.w))
-                                             : "memory");
-                            }
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    // all rows of the unit learn of it, and all of the tile is clean before any of them goes on
-                    if (flags & kTree) dirty |= two ? softmax_any<2 * kTileM>(odd) : softmax_any<kTileM>(odd);
-                    __syncwarp();
+                    see[w] = tile.words[w] & (flags & kTree ? tree_bits[w] : 0xffffffffu);
+                    seen |= see[w] != 0;
                 }
             } else {
                 seen = true;
@@ -841,6 +824,45 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 tmem_st16(s_addr + 16 * q, w);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (!(flags & kPlain)) {
+                // What must not meet a weight of zero: the rows past the end of a partly used box become
+                // zeros, and values that are not finite leave drafted rows, which some rows do not see.
+                // Both streams share the work, and none of their rows goes on before it is done.  (The
+                // scores of tile t are there, so the slot's last V has been used up and the parity of
+                // `full` is that of V(t).)
+                const int valid = meta[mt].valid, box_rows = flags & kTree ? kTreeBox : p.block_size;
+                if ((flags & kTree) || (valid & (box_rows - 1))) {
+                    const int it = v_item(t);
+                    ok = tree_wait(full + it % kSlots, (it / kSlots) & 1, p.err_flag);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    const uint32_t v0 = smem_addr(ring) + it % kSlots * C::kTileBytes;
+                    const int end = (valid + box_rows - 1) & -box_rows;
+                    const bool two = STREAMS == 2 && (flags & kTwo);
+                    const int at = two ? threadIdx.x : r, rows = two ? 32 : 16;  // a row is eight chunks
+                    bool odd = false;
+#pragma unroll 1
+                    for (int row = (flags & kTree ? 0 : valid) + (at >> 3); row < end; row += rows) {
+#pragma unroll
+                        for (int x = 0; x < C::kBoxes; ++x) {
+                            const uint32_t addr = v0 + x * C::kBoxBytes + row * 128 + (at & 7) * 16;
+                            uint4 v = lds128(addr);
+                            const bool bad = not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w);
+                            if (row >= valid)
+                                v = make_uint4(0u, 0u, 0u, 0u);
+                            else if (bad)
+                                v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+                            else
+                                continue;
+                            odd |= row < valid;
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+                                         "r"(v.z), "r"(v.w)
+                                         : "memory");
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    dirty |= two ? softmax_any<2 * kTileM>(odd) : softmax_any<kTileM>(odd);
+                }
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -854,9 +876,41 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             }
 
             // ---- the piece's output ----
-            const TileMeta tile = meta[mt];
+            const int first = meta[mt].first, nodes = meta[mt].nodes, dest = meta[mt].dest, h = meta[mt].h;
+            const int node_base = meta[mt].node0 + s * tile_nodes;
             __syncwarp();
             if (lane == 0) mbar_arrive(meta_free + mt);
+            // Rows leave through shared memory: a lane holds a row, but four lanes store 64 bytes of one,
+            // eight rows at a time.  Chunk k of row w is at k ^ (w / 2 % 4): no bank conflicts either way.
+            const bool whole = dest < 0;
+            const uint32_t mine = smem_addr(stage) + warp * 2048;
+            const uint32_t put = mine + lane * 64, put_x = (lane >> 1) & 3;
+            const uint32_t get = mine + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+            const int64_t state = (int64_t)dest * (STREAMS * kTileM) + s * kTileM;  // of the stream's row 0
+            char *dst[4];  // of the rows this lane stores (NULL: past the last node)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int row = (warp & 3) * 32 + 8 * k + (lane >> 2), n = node_base + (row >> p.group_shift);
+                dst[k] = n >= nodes ? nullptr
+                         : whole ? reinterpret_cast<char *>(
+                                       p.out + ((int64_t)(first + n) * p.q_heads + (h * G + (row & (G - 1)))) * HEAD_DIM)
+                                 : reinterpret_cast<char *>(p.part_o + (state + row) * HEAD_DIM);
+                if (dst[k]) dst[k] += (lane & 3) * 16;
+            }
+            auto store64 = [&](int bytes, const uint4 (&v)[4]) {
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(put + ((k ^ put_x) << 4)), "r"(v[k].x),
+                                 "r"(v[k].y), "r"(v[k].z), "r"(v[k].w)
+                                 : "memory");
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // row 8 k + lane / 4: its swizzle is that of row lane / 4
+                    const uint4 x = lds128(get + k * 512);
+                    if (dst[k]) *reinterpret_cast<uint4 *>(dst[k] + bytes) = x;
+                }
+            };
             ok = tree_wait(o_done + s, pieces++ & 1, p.err_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -868,33 +922,6 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             else if (m == -INFINITY && seen)
                 l = NAN;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool whole = tile.dest < 0;
-            const int64_t state = (int64_t)tile.dest * (STREAMS * kTileM) + s * kTileM;  // of the stream's row 0
-            // Rows leave through shared memory: a lane holds a row, but four lanes store 64 bytes of one,
-            // eight rows at a time.  Chunk k of row w is at k ^ (w / 2 % 4): no bank conflicts either way.
-            const uint32_t mine = smem_addr(stage) + warp * 2048;
-            const int w0 = (warp & 3) * 32;  // the warp's first row of the stream
-            const int node_base = tile.place / p.kv_heads + s * tile_nodes;
-            auto store64 = [&](int col, const uint4 (&v)[4]) {
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)),
-                                 "r"(v[k].x), "r"(v[k].y), "r"(v[k].z), "r"(v[k].w)
-                                 : "memory");
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int w = 8 * k + (lane >> 2), row = w0 + w;
-                    const uint4 x = lds128(mine + w * 64 + (((lane & 3) ^ ((w >> 1) & 3)) << 4));
-                    const int n = node_base + (row >> p.group_shift);
-                    if (n >= tile.nodes) continue;
-                    char *dst = whole ? reinterpret_cast<char *>(p.out) +
-                                            (((int64_t)(tile.first + n) * p.q_heads + h * G + (row & (G - 1))) * HEAD_DIM + col) * 2
-                                      : reinterpret_cast<char *>(p.part_o) + ((state + row) * HEAD_DIM + col) * 4;
-                    *reinterpret_cast<uint4 *>(dst + (lane & 3) * 16) = x;
-                }
-            };
 #pragma unroll 1
             for (int q = 0; q < HEAD_DIM / 32; ++q) {
                 float o[32];
@@ -902,11 +929,11 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 tmem_ld32(o_addr + 32 * q, o);
                 tmem_wait_ld();
                 if (live && dirty) {  // the values that were kept out of the product
-                    for (int k = 0; k < tile.nodes; ++k) {
-                        const bool sees = p.masks ? (__ldg(p.masks + (int64_t)(tile.first + node) * p.words + (k >> 5)) >> (k & 31)) & 1
+                    for (int k = 0; k < nodes; ++k) {
+                        const bool sees = p.masks ? (__ldg(p.masks + (int64_t)(first + node) * p.words + (k >> 5)) >> (k & 31)) & 1
                                                   : k <= node;
                         if (!sees) continue;
-                        const uint16_t *src = p.v_tree + (int64_t)(tile.first + k) * p.v_stride + h * HEAD_DIM + 32 * q;
+                        const uint16_t *src = p.v_tree + (int64_t)(first + k) * p.v_stride + h * HEAD_DIM + 32 * q;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const uint32_t bits = (uint32_t)src[i] << 16;
@@ -922,7 +949,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                     for (int i = 0; i < 4; ++i)
                         v[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
                                           pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-                    store64(32 * q, v);
+                    store64(64 * q, v);
                 } else {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -930,7 +957,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                         for (int i = 0; i < 4; ++i)
                             v[i] = make_uint4(__float_as_uint(o[16 * half + 4 * i]), __float_as_uint(o[16 * half + 4 * i + 1]),
                                               __float_as_uint(o[16 * half + 4 * i + 2]), __float_as_uint(o[16 * half + 4 * i + 3]));
-                        store64(32 * q + 16 * half, v);
+                        store64(128 * q + 64 * half, v);
                     }
                 }
             }
