@@ -29,11 +29,13 @@
 //    weight: O stays in TMEM and is rescaled a few times in a row's life instead of
 //    once a tile.  fp32 holds weights up to 2^8 as well as up to 1, and the
 //    quotient at the end does not depend on which reference was used.
-//  * STREAMS = 1 (up to 128 query rows, bound by HBM): 64-token tiles with two score
-//    buffers, two CTAs on an SM.  STREAMS = 2 (more rows, bound by the products and
-//    the exponentials): two groups of 128 rows share each K and V tile of 128 tokens
-//    and take turns on the tensor cores; an mma of N = 64 takes as long as one of
-//    N = 128 (65 cycles measured), so the longer tile halves their number.
+//  * STREAMS = 1 (up to 128 query rows, bound by HBM): two CTAs on an SM.  STREAMS = 2
+//    (more rows, bound by the products and the exponentials): two groups of 128 rows
+//    share each K and V tile, each with a thread of its own for the products.
+//  * Tiles of 64 tokens with two score buffers: the scores of the next tile are made
+//    while this one goes through the softmax.  One buffer of 128 tokens needs half
+//    the mma instructions (65 cycles each at N = 64 as at N = 128), but then scores,
+//    softmax and product of a stream follow one another: 6500 cycles for 128 tokens.
 //  * What a row does not see has no part in it.  Scores are replaced, not added
 //    to; V rows past the sequence's end are zeroed in shared memory before they meet
 //    a weight of zero; non-finite values of drafted V rows (which some rows see and
@@ -53,22 +55,22 @@ constexpr float kMaxRise = 8.0f;   // log2 of the largest weight before the refe
 
 template <int HEAD_DIM, int STREAMS>
 struct TreeCfg {
-    static constexpr int kTileN = STREAMS == 1 ? 64 : 128;     // tokens of one tile
-    static constexpr int kBufs = 128 / kTileN;                 // score buffers of a stream
+    static constexpr int kTileN = 64;                          // tokens of one tile
+    static constexpr uint32_t kBufs = 128 / kTileN;            // score buffers of a stream
     static constexpr int kBoxes = HEAD_DIM / 64;               // 128-byte wide column boxes
     static constexpr int kBoxBytes = kTileN * 128;             // one box of a K or V tile
     static constexpr int kTileBytes = kBoxes * kBoxBytes;
     static constexpr int kQBoxBytes = kTileM * 128;
     static constexpr int kQBytes = kBoxes * kQBoxBytes;        // one stream's queries
-    static constexpr int kSlots = HEAD_DIM == 64 ? 8 : 4;      // ring depth
-    static constexpr int kMetas = 16;                          // tile descriptions
+    static constexpr uint32_t kSlots = STREAMS * (HEAD_DIM == 64 ? 8 : 4);  // ring depth
+    static constexpr uint32_t kMetas = 16;                     // tile descriptions
     static constexpr int kCtasPerSm = STREAMS == 1 ? 2 : 1;
     static constexpr int kSoftmaxWarps = 4 * STREAMS;
     static constexpr int kThreads = (kSoftmaxWarps + 1 + STREAMS) * 32;  // + producer, product warps
     // TMEM of one stream: the score buffers (P in the first half of each), then O.
     static constexpr int kStreamCols = 128 + 128;
     static constexpr int kCols = STREAMS * kStreamCols;
-    static constexpr int kBars = 2 * kSlots + 2 * kMetas + STREAMS * (2 * kBufs + 5);
+    static constexpr uint32_t kBars = 2 * kSlots + 2 * kMetas + STREAMS * (2 * kBufs + 5);
     static constexpr int kDataBytes = STREAMS * kQBytes + kSlots * kTileBytes;
     // Each softmax warp turns its rows of the output into whole 64-byte pieces here.
     static constexpr int kStageBytes = kSoftmaxWarps * 2048;
@@ -216,18 +218,25 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ bool tree_wait(uint64_t *bar, uint32_t parity, int32_t *flag) {
     return mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, flag);
 }
+// Barriers kept in a ring: use n of it has its place and its parity (ring lengths are powers of two).
+template <uint32_t N>
+__device__ __forceinline__ bool ring_wait(uint64_t *bars, uint32_t n, int32_t *flag) {
+    return tree_wait(bars + (n & (N - 1)), (n / N) & 1, flag);
+}
 
-// A barrier of the softmax warps of one CTA that also ORs a predicate over them.
-template <int THREADS>
+// A barrier of the softmax warps of `STREAMS` streams that also ORs a predicate over them.  Each number of
+// streams has a barrier of its own: the second stream skips tiles without rows of its own and may wait at
+// the next common one while the first is still at a barrier alone.
+template <int STREAMS>
 __device__ __forceinline__ bool softmax_any(bool mine) {
     uint32_t any;
     __syncwarp();  // an aligned barrier wants whole warps
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.aligned.pred q, 1, %2, p;\n\t"
+        "barrier.cta.red.or.aligned.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
-        : "r"((uint32_t)mine), "n"(THREADS)
+        : "r"((uint32_t)mine), "n"(STREAMS), "n"(STREAMS * kTileM)
         : "memory");
     return any != 0;
 }
@@ -386,7 +395,8 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap kt_map,
                 const __grid_constant__ CUtensorMap vt_map, const TreeParams p) {
     using C = TreeCfg<HEAD_DIM, STREAMS>;
-    constexpr int kTileN = C::kTileN, kBufs = C::kBufs, kSlots = C::kSlots;
+    constexpr int kTileN = C::kTileN;
+    constexpr uint32_t kBufs = C::kBufs, kSlots = C::kSlots;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -442,8 +452,8 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
 
     // The tiles of this CTA are numbered through all its pieces.  Items of the ring, in their order:
     // K of the first kBufs tiles, then V(0) K(kBufs) V(1) K(kBufs + 1) ...
-    auto k_item = [](int t) { return t < kBufs ? t : 2 * t - kBufs + 1; };
-    auto v_item = [](int t) { return 2 * t + kBufs; };
+    auto k_item = [](uint32_t t) { return t < kBufs ? t : 2 * t - kBufs + 1; };
+    auto v_item = [](uint32_t t) { return 2 * t + kBufs; };
 
     if (warp == C::kSoftmaxWarps) {
         // ---------------- producer: units, block-table dereference, TMA ----------------
@@ -522,15 +532,14 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             return t;
         };
         int landed = -1;  // lane s: the last item loaded into slot s
-        auto take_slot = [&](int it) {
-            bool ok = true;
-            if (it >= kSlots) ok = tree_wait(empty + it % kSlots, (it / kSlots - 1) & 1, p.err_flag);
+        auto take_slot = [&](uint32_t it) {
+            const bool ok = it < kSlots || ring_wait<kSlots>(empty, it - kSlots, p.err_flag);
             return (bool)__all_sync(0xffffffffu, ok);
         };
-        auto load = [&](const Tile &t, bool is_k, int it) {
-            const int slot = it % kSlots;
+        auto load = [&](const Tile &t, bool is_k, uint32_t it) {
+            const uint32_t slot = it & (kSlots - 1);
             uint8_t *dst = ring + slot * C::kTileBytes;
-            if (lane == slot) landed = it;
+            if (lane == (int)slot) landed = (int)it;
             // V past the end is read from outside of the tensor, which gives zeros: whatever the ring held
             // must not meet a weight of zero.  (The rest of a partly used box is zeroed by the softmax warps.)
             if (t.flags & kTree) {
@@ -558,17 +567,17 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         };
         // Tiles are drawn ahead of their loads, so that table entries are there when they are needed.
         Tile t0 = next_tile(), t1 = next_tile(), older = t0;
-        int n = INT_MAX;  // tiles of this CTA, once known
-        for (int t = 0;; ++t) {
-            if (n == INT_MAX) {
+        uint32_t n = UINT32_MAX;  // tiles of this CTA, once known
+        for (uint32_t t = 0;; ++t) {
+            if (n == UINT32_MAX) {
                 if (!take_slot(k_item(t))) break;
                 const uint32_t holes = __ballot_sync(0xffffffffu, t0.mine && box == 0 && (t0.id < 0 || t0.id >= p.num_blocks));
                 if (holes) {
                     if (lane == 0) raise_flag(p.err_flag, PA_FLAG_BAD_BLOCK);
                     t0.flags &= ~kPlain;
                 }
-                const int mt = t % C::kMetas;
-                const bool free = t < C::kMetas || tree_wait(meta_free + mt, (t / C::kMetas - 1) & 1, p.err_flag);
+                const uint32_t mt = t & (C::kMetas - 1);
+                const bool free = t < C::kMetas || ring_wait<C::kMetas>(meta_free, t - C::kMetas, p.err_flag);
                 if (!__all_sync(0xffffffffu, free)) break;
                 if (lane == 0) {
                     TileMeta &d = meta[mt];
@@ -597,9 +606,9 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 else
                     load(t0, true, k_item(t));
             }
-            const int u = t - (kBufs - 1);  // the tile whose V comes next
-            if (u >= n) break;
-            if (u >= 0) {
+            const uint32_t u = t - (kBufs - 1);  // the tile whose V comes next
+            if (t >= kBufs - 1) {
+                if (u >= n) break;
                 if (!take_slot(v_item(u))) break;
                 load(kBufs == 1 ? t0 : older, false, v_item(u));
             }
@@ -608,7 +617,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             t1 = next_tile();
         }
         // Every copy has landed before the CTA ends (it has, unless a wait ran out).
-        if (lane < kSlots && landed >= 0) mbar_wait_bounded(full + lane, (landed / kSlots) & 1, p.err_flag);
+        if (lane < (int)kSlots && landed >= 0) mbar_wait_bounded(full + lane, ((uint32_t)landed / kSlots) & 1, p.err_flag);
     } else if (warp > C::kSoftmaxWarps) {
         // ---------------- products, issued by one thread for each stream ----------------
         // O += P V of tile t - kBufs, then S = Q K^T of tile t.
@@ -621,63 +630,64 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             const uint64_t k_desc = umma_desc_k_sw128(smem_addr(ring));
             const uint64_t v_desc = umma_desc_mn_sw128(smem_addr(ring), C::kBoxBytes);
             const uint32_t base = tmem + s * C::kStreamCols;
-            int scored = 0, added = 0;      // tiles whose scores / products were issued
-            int pieces_q = 0, pieces_o = 0;
-            int queue[kBufs] = {};          // flags of the tiles between the two
-            auto wait_item = [&](int it) { return tree_wait(full + it % kSlots, (it / kSlots) & 1, p.err_flag); };
+            uint32_t scored = 0, added = 0;  // tiles whose scores / products were issued
+            uint32_t pieces_q = 0, pieces_o = 0;
+            int queue[kBufs] = {};           // flags of the tiles between the two
+            auto wait_item = [&](uint32_t it) { return ring_wait<kSlots>(full, it, p.err_flag); };
             bool ok = true, over = false;
-            for (int t = 0; ok; ++t) {
+            for (uint32_t t = 0; ok; ++t) {
                 if (t >= kBufs) {
-                    const int f = queue[0], it = v_item(t - kBufs);
+                    const int f = queue[0];
+                    const uint32_t it = v_item(t - kBufs), slot = it & (kSlots - 1);
                     if (f & kEnd) break;
                     if (!(ok = wait_item(it))) break;
                     if (s == 0 || (f & kTwo)) {
-                        const int g = added++;
-                        if (!(ok = tree_wait(p_full + kBufs * s + g % kBufs, (g / kBufs) & 1, p.err_flag))) break;
+                        const uint32_t g = added++;
+                        if (!(ok = ring_wait<kBufs>(p_full + kBufs * s, g, p.err_flag))) break;
                         // a new piece overwrites O: the last one's has to have been read
                         if ((f & kFirst) && pieces_o++ > 0 && !(ok = tree_wait(o_free + s, pieces_o & 1, p.err_flag))) break;
                         tc_fence_after();
-                        const uint64_t vd = v_desc + (uint32_t)(it % kSlots * (C::kTileBytes / 16));
-                        const uint32_t a = base + g % kBufs * kTileN;
+                        const uint64_t vd = v_desc + slot * (C::kTileBytes / 16);
+                        const uint32_t a = base + (g & (kBufs - 1)) * kTileN;
 #pragma unroll
                         for (int i = 0; i < kTileN / 16; ++i)
                             umma_bf16_ts(base + 128, a + 8 * i, vd + i * (2048 / 16), kPvDesc, !(f & kFirst) || i > 0);
                         umma_commit(pv_done + s);
                         if (f & kLast) umma_commit(o_done + s);
-                        umma_commit(empty + it % kSlots);
+                        umma_commit(empty + slot);
                     } else {
-                        mbar_arrive(empty + it % kSlots);
+                        mbar_arrive(empty + slot);
                     }
                 }
                 int f = kEnd;
                 if (!over) {
-                    if (!(ok = tree_wait(meta_full + t % C::kMetas, (t / C::kMetas) & 1, p.err_flag))) break;
-                    f = *const_cast<volatile int *>(&meta[t % C::kMetas].flags);
+                    if (!(ok = ring_wait<C::kMetas>(meta_full, t, p.err_flag))) break;
+                    f = *const_cast<volatile int *>(&meta[t & (C::kMetas - 1)].flags);
                     over = f & kEnd;
                 }
                 if (!over) {
-                    const int it = k_item(t);
+                    const uint32_t it = k_item(t), slot = it & (kSlots - 1);
                     if (!(ok = wait_item(it))) break;
                     if (s == 0 || (f & kTwo)) {
                         if ((f & kFirst) && !(ok = tree_wait(q_full + s, pieces_q++ & 1, p.err_flag))) break;
-                        const int g = scored++;
+                        const uint32_t g = scored++;
                         // the new scores take the place of an earlier tile's P: its product has to be done
                         if (g >= kBufs && !(ok = tree_wait(pv_done + s, (g - kBufs) & 1, p.err_flag))) break;
                         tc_fence_after();
-                        const uint64_t kd = k_desc + (uint32_t)(it % kSlots * (C::kTileBytes / 16));
-                        const uint32_t d = base + g % kBufs * kTileN;
+                        const uint64_t kd = k_desc + slot * (C::kTileBytes / 16);
+                        const uint32_t d = base + (g & (kBufs - 1)) * kTileN;
 #pragma unroll
                         for (int i = 0; i < HEAD_DIM / 16; ++i)
                             umma_bf16_ss(d, q_desc + ((i >> 2) * C::kQBoxBytes + (i & 3) * 32) / 16,
                                          kd + ((i >> 2) * C::kBoxBytes + (i & 3) * 32) / 16, kQkDesc, i > 0);
-                        umma_commit(s_full + kBufs * s + g % kBufs);
-                        umma_commit(empty + it % kSlots);
+                        umma_commit(s_full + kBufs * s + (g & (kBufs - 1)));
+                        umma_commit(empty + slot);
                     } else {
-                        mbar_arrive(empty + it % kSlots);
+                        mbar_arrive(empty + slot);
                     }
                 }
 #pragma unroll
-                for (int x = 0; x + 1 < kBufs; ++x) queue[x] = queue[x + 1];
+                for (uint32_t x = 0; x + 1 < kBufs; ++x) queue[x] = queue[x + 1];
                 queue[kBufs - 1] = f;
             }
             umma_commit(drained + s);
@@ -696,10 +706,10 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
 
         // One thread of each stream loads its queries: the first piece's at once, the next one's when the
         // last scores of a piece are there, while their softmax and the piece's output are still to come.
-        int q_loads = 0;
-        auto load_queries = [&](int t) {
-            if (!tree_wait(meta_full + t % C::kMetas, (t / C::kMetas) & 1, p.err_flag)) return;
-            const volatile TileMeta &m = meta[t % C::kMetas];
+        uint32_t q_loads = 0;
+        auto load_queries = [&](uint32_t t) {
+            if (!ring_wait<C::kMetas>(meta_full, t, p.err_flag)) return;
+            const volatile TileMeta &m = meta[t & (C::kMetas - 1)];
             const int f = m.flags, row = m.first + m.node0 + s * tile_nodes, head = m.h * G;
             if ((f & kEnd) || (s == 1 && !(f & kTwo))) return;
             mbar_arrive_expect_tx(q_full + s, C::kQBytes);
@@ -710,15 +720,15 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         if ((warp & 3) == 0 && lane == 0) load_queries(0);
 
         constexpr int kWords = kTileN / 32;
-        int g = 0, pieces = 0;  // tiles and pieces of this stream so far
-        int node = 0;           // of this thread's row
+        uint32_t g = 0, pieces = 0;  // tiles and pieces of this stream so far
+        int node = 0;                // of this thread's row
         bool live = false, seen = false, dirty = false;
         uint32_t tree_bits[kWords] = {};  // the row's mask of the first drafted tile
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int t = 0;; ++t) {
-            const int mt = t % C::kMetas;
-            ok = tree_wait(meta_full + mt, (t / C::kMetas) & 1, p.err_flag);
+        for (uint32_t t = 0;; ++t) {
+            const uint32_t mt = t & (C::kMetas - 1);
+            ok = ring_wait<C::kMetas>(meta_full, t, p.err_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             const int flags = meta[mt].flags;
             if (flags & kEnd) break;
@@ -743,8 +753,8 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                                    : w < p.words ? (uint32_t)__ldg(p.masks + (int64_t)(tile.first + node) * p.words + w)
                                                  : 0u;
             }
-            const int buf = g % kBufs;
-            ok = tree_wait(s_full + kBufs * s + buf, (g / kBufs) & 1, p.err_flag);
+            const uint32_t buf = g & (kBufs - 1);
+            ok = ring_wait<kBufs>(s_full + kBufs * s, g, p.err_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             if ((flags & kLast) && (warp & 3) == 0 && lane == 0) load_queries(t + 1);
             // the tokens of the tile that this row sees
@@ -832,10 +842,10 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 // `full` is that of V(t).)
                 const int valid = meta[mt].valid, box_rows = flags & kTree ? kTreeBox : p.block_size;
                 if ((flags & kTree) || (valid & (box_rows - 1))) {
-                    const int it = v_item(t);
-                    ok = tree_wait(full + it % kSlots, (it / kSlots) & 1, p.err_flag);
+                    const uint32_t it = v_item(t);
+                    ok = ring_wait<kSlots>(full, it, p.err_flag);
                     if (!__all_sync(0xffffffffu, ok)) break;
-                    const uint32_t v0 = smem_addr(ring) + it % kSlots * C::kTileBytes;
+                    const uint32_t v0 = smem_addr(ring) + (it & (kSlots - 1)) * C::kTileBytes;
                     const int end = (valid + box_rows - 1) & -box_rows;
                     const bool two = STREAMS == 2 && (flags & kTwo);
                     const int at = two ? threadIdx.x : r, rows = two ? 32 : 16;  // a row is eight chunks
@@ -860,7 +870,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                         }
                     }
                     fence_proxy_async_smem();
-                    dirty |= two ? softmax_any<2 * kTileM>(odd) : softmax_any<kTileM>(odd);
+                    dirty |= two ? softmax_any<2>(odd) : softmax_any<1>(odd);
                 }
             }
             tmem_wait_st();
