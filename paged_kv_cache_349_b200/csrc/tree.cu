@@ -71,16 +71,18 @@ int tree_share(int max_seq_len, int requested) {
     return max_seq_len <= 2 * share ? -1 : share;
 }
 
-// Workspace: two states for each CTA, of a unit that began before it and of one that ends after it.
+// Workspace: two states for each CTA, of a unit that began before it and of one that ends after it,
+// then what there is to join.
 struct TreeLayout {
-    size_t ml, total;
+    size_t ml, joins, total;
 };
 
 TreeLayout tree_layout(int ctas, int streams, int head_dim) {
     const size_t rows = (size_t)ctas * 2 * streams * kTileM;
     TreeLayout l{};
     l.ml = rows * head_dim * 4;
-    l.total = l.ml + rows * 8;
+    l.joins = l.ml + rows * 8;
+    l.total = l.joins + (size_t)ctas * sizeof(TreeJoin);
     return l;
 }
 
@@ -195,6 +197,7 @@ int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tre
         if (!workspace || workspace_bytes < l.total || !pa::aligned16(workspace)) return PA_ERR_INVALID_ARG;
         p.part_o = static_cast<float *>(workspace);
         p.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + l.ml);
+        p.joins = reinterpret_cast<pa::TreeJoin *>(static_cast<char *>(workspace) + l.joins);
     }
     // row numbers and places of a unit are int32
     if ((int64_t)max_nodes * num_q_heads > INT32_MAX / 2 || (int64_t)max_blocks_per_seq * block_size > INT32_MAX / 2)

@@ -74,24 +74,31 @@ struct TreeCfg {
     static constexpr int kDataBytes = STREAMS * kQBytes + kSlots * kTileBytes;
     // Each softmax warp turns its rows of the output into whole 64-byte pieces here.
     static constexpr int kStageBytes = kSoftmaxWarps * 2048;
-    static constexpr int kTailBytes = kStageBytes + kMetas * 48 + kBars * 8 + 32 * 8 + 2 * 16 + 16;
+    static constexpr int kTailBytes = kStageBytes + kMetas * 48 + kBars * 8 + 32 * 8 + 2 * 16 + 16 + 64 /* TreeSpot */;
     static constexpr int kSmemBytes = 1024 /* align slack */ + kDataBytes + kTailBytes;
     static_assert(kCtasPerSm * kCols <= 512, "TMEM columns of an SM");
     static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
-    // What a unit costs besides its tiles, and the shortest pieces worth cutting off, in tiles.
-    static constexpr int kUnitCost = 128 / kTileN;
-    static constexpr int kSnap = 128 / kTileN;
+    // What a unit costs besides its tiles (its output, and tiles that are not whole: 4 us measured, a tile
+    // 1.3 us), and the shortest pieces worth cutting off, in tiles.
+    static constexpr int kUnitCost = 3;
+    static constexpr int kSnap = 2;
 };
 
 // Where a CTA's share begins: tile `tile` of unit `unit` of sequence `b` (b = batch: nowhere).
 struct TreeMark {
-    int b, unit, tile, pad;
+    int b, unit, tile;
+};
+
+// What the second kernel joins: the pieces of the unit whose first cut is where a CTA begins (0: none).
+struct __align__(16) TreeJoin {
+    int pieces, first, nodes, node0, h, pad[3];
 };
 
 struct TreeParams {
     uint16_t *out;             // [T, Hq, d] bf16
     float *part_o;             // [CTAs, 2, rows of a unit, d]: states of units that are cut (NULL: none is)
     float *part_ml;            // [CTAs, 2, rows of a unit, 2]
+    TreeJoin *joins;           // [CTAs]
     const uint16_t *v_tree;
     const int32_t *tables, *lens, *cu, *masks;
     int32_t *err_flag;
@@ -333,6 +340,12 @@ __device__ __forceinline__ TreeLine tree_line(const TreeParams &p, int ctas, int
     return n;
 }
 
+// What is left of it for one CTA: where the unit of its first mark begins.
+struct TreeSpot {
+    int64_t begin;
+    TreeLine line;
+};
+
 // Where cut i lies on the line.
 __device__ __forceinline__ int64_t tree_cut(const TreeLine &n, int i) {
     if (i >= n.count) return n.total;
@@ -344,7 +357,7 @@ template <int HEAD_DIM, int STREAMS>
 __device__ __forceinline__ TreeMark tree_mark(const TreeParams &p, const TreeUnits &u, int b, int64_t at) {
     using C = TreeCfg<HEAD_DIM, STREAMS>;
     const int weight = u.tiles + C::kUnitCost;
-    TreeMark m{b, at <= INT32_MAX ? (int)at / weight : (int)(at / weight), 0, 0};
+    TreeMark m{b, at <= INT32_MAX ? (int)at / weight : (int)(at / weight), 0};
     const int tile = (int)(at - (int64_t)m.unit * weight) - C::kUnitCost;
     if (p.part_o ? tile > u.tiles - C::kSnap : 2 * tile >= u.tiles)
         ++m.unit;
@@ -355,13 +368,14 @@ __device__ __forceinline__ TreeMark tree_mark(const TreeParams &p, const TreeUni
 
 // The marks of cuts i and i + 1.  Every CTA computes the same cuts from the lengths alone.
 template <int HEAD_DIM, int STREAMS, int THREADS>
-__device__ __forceinline__ void tree_marks(const TreeParams &p, int ctas, int i, int64_t *scan, TreeMark *mark, bool report) {
+__device__ __forceinline__ void tree_marks(const TreeParams &p, int ctas, int i, int64_t *scan, TreeMark *mark,
+                                           TreeSpot *spot, bool report) {
     using C = TreeCfg<HEAD_DIM, STREAMS>;
     const TreeLine n = tree_line<HEAD_DIM, STREAMS, THREADS>(p, ctas, scan, report);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         int64_t at = tree_cut(n, i + k);
-        if (threadIdx.x == 0 && at >= n.total) mark[k] = TreeMark{p.batch, 0, 0, 0};
+        if (threadIdx.x == 0 && at >= n.total) mark[k] = TreeMark{p.batch, 0, 0};
         at -= n.before;
         if (at < 0 || at >= n.mine) continue;
         for (int b = n.b0; b < n.b1; ++b) {
@@ -369,6 +383,10 @@ __device__ __forceinline__ void tree_marks(const TreeParams &p, int ctas, int i,
             const int64_t weight = (int64_t)(u.chunks * p.kv_heads) * (u.tiles + C::kUnitCost);
             if (at < weight) {
                 mark[k] = tree_mark<HEAD_DIM, STREAMS>(p, u, b, at);
+                if (k == 0) {
+                    spot->line = n;
+                    spot->begin = tree_cut(n, i) - at + (int64_t)mark[k].unit * (u.tiles + C::kUnitCost);
+                }
                 break;
             }
             at -= weight;
@@ -416,7 +434,9 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
     uint64_t *o_done = pv_done + STREAMS;         // [stream]: a piece's last tile has
     uint64_t *o_free = o_done + STREAMS;          // [stream]: a piece's O has been read
     uint64_t *drained = o_free + STREAMS;         // [stream]: every product has completed
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + STREAMS);
+    TreeSpot *spot = reinterpret_cast<TreeSpot *>(drained + STREAMS);
+    static_assert(sizeof(TreeSpot) <= 64, "fits its place");
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(spot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group;
@@ -445,7 +465,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         tmem_relinquish();
         tc_fence_before();
     }
-    tree_marks<HEAD_DIM, STREAMS, C::kThreads>(p, gridDim.x, blockIdx.x, scan, mark, blockIdx.x == 0);  // synchronises
+    tree_marks<HEAD_DIM, STREAMS, C::kThreads>(p, gridDim.x, blockIdx.x, scan, mark, spot, blockIdx.x == 0);  // synchronises
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     if (p.part_o) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -615,6 +635,31 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             older = t0;
             t0 = t1;
             t1 = next_tile();
+        }
+        // If this CTA begins at the first cut inside a unit: how many pieces that unit has.
+        if (p.part_o && lane == 0) {
+            TreeJoin j{0, 0, 0, 0, 0, {}};
+            const TreeMark at = mark[0];
+            if (at.b < p.batch && at.tile != 0) {
+                const TreeSeq q = tree_seq(p, at.b);
+                const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, q);
+                auto inside = [&](int i) {  // cut i is one of this unit
+                    if (i >= spot->line.count) return false;
+                    const int64_t x = tree_cut(spot->line, i) - spot->begin;
+                    if (x < 0 || x >= u.tiles + C::kUnitCost) return false;
+                    const TreeMark m = tree_mark<HEAD_DIM, STREAMS>(p, u, at.b, x);
+                    return m.unit == 0 && m.tile != 0;
+                };
+                if (!inside((int)blockIdx.x - 1)) {
+                    j.pieces = 2;
+                    while (inside((int)blockIdx.x + j.pieces - 1)) ++j.pieces;
+                    j.first = q.first;
+                    j.nodes = q.nodes;
+                    j.h = at.unit / u.chunks;
+                    j.node0 = (at.unit - j.h * u.chunks) * (STREAMS * tile_nodes);
+                }
+            }
+            p.joins[blockIdx.x] = j;
         }
         // Every copy has landed before the CTA ends (it has, unless a wait ran out).
         if (lane < (int)kSlots && landed >= 0) mbar_wait_bounded(full + lane, ((uint32_t)landed / kSlots) & 1, p.err_flag);
@@ -993,62 +1038,21 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
 //   out = sum_p 2^(m_p - M) l_p o_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p.
 // CTA (i, y): if cut i + 1 is the first one inside its unit, rows [32 y, 32 y + 32) of that unit.  The
 // piece before the first cut is CTA i's second state, the pieces after the cuts are the first states of
-// the CTAs that begin there.  Which cuts those are follows from the lengths, so all of it is worked out
-// while the attention still runs; four rows of a warp are in flight at once.
+// the CTAs that begin there.  Four rows of a warp are in flight at once.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinRows = 32;
 
 template <int HEAD_DIM, int STREAMS>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams p) {
-    using C = TreeCfg<HEAD_DIM, STREAMS>;
     constexpr int V = HEAD_DIM / 32, R = kJoinRows / kJoinWarps;
     constexpr int kRows = STREAMS * kTileM;
-    __shared__ int64_t scan[32];
-    __shared__ TreeMark s_at;
-    __shared__ int s_pieces;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = blockIdx.x + 1, ctas = gridDim.x + 1;
-    if (threadIdx.x == 0) s_pieces = 0;
-    const TreeLine n = tree_line<HEAD_DIM, STREAMS, kJoinWarps * 32>(p, ctas, scan, false);
-    int64_t at = tree_cut(n, first) - n.before;
-    if (at >= 0 && at < n.mine && first < n.count) {  // this thread's sequences hold the cut
-        int64_t begin = n.before;
-        for (int b = n.b0; b < n.b1; ++b) {
-            const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, tree_seq(p, b));
-            const int weight = u.tiles + C::kUnitCost;
-            const int64_t all = (int64_t)(u.chunks * p.kv_heads) * weight;
-            if (at >= all) {
-                at -= all;
-                begin += all;
-                continue;
-            }
-            const TreeMark m = tree_mark<HEAD_DIM, STREAMS>(p, u, b, at);
-            auto inside = [&](int i) {  // cut i is one of this unit
-                if (i >= n.count) return false;
-                const int64_t x = tree_cut(n, i) - begin;
-                if (x < (int64_t)m.unit * weight || x >= (int64_t)(m.unit + 1) * weight) return false;
-                const TreeMark y = tree_mark<HEAD_DIM, STREAMS>(p, u, b, x);
-                return y.unit == m.unit && y.tile != 0;
-            };
-            if (m.tile != 0 && !inside(first - 1)) {
-                int pieces = 2;
-                while (inside(first + pieces - 1)) ++pieces;
-                s_at = m;
-                s_pieces = pieces;
-            }
-            break;
-        }
-    }
-    __syncthreads();
-    const int pieces = s_pieces;
-    if (pieces == 0) return;
-    const TreeSeq seq = tree_seq(p, s_at.b);
-    const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, seq);
-    const int h = s_at.unit / u.chunks;
-    const int node0 = (s_at.unit - h * u.chunks) * (STREAMS * kTileM >> p.group_shift);
-    const int r0 = blockIdx.y * kJoinRows + warp * R;
-    if (node0 + (r0 >> p.group_shift) >= seq.nodes) return;
+    const int first = blockIdx.x + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const TreeJoin j = p.joins[first];
+    const int node0 = j.node0, pieces = j.pieces, h = j.h;
+    const int r0 = blockIdx.y * kJoinRows + warp * R;
+    if (pieces == 0 || node0 + (r0 >> p.group_shift) >= j.nodes) return;
     // state of piece k: 2 * first - 1, then 2 * first, 2 * first + 2, ...
     auto state = [&](int k) { return (int64_t)(k == 0 ? 2 * first - 1 : 2 * (first + k - 1)) * kRows + r0; };
     float M[R], den[R], none[R], acc[R][V];
@@ -1093,9 +1097,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int row = r0 + r, node = node0 + (row >> p.group_shift);
-        if (node >= seq.nodes) break;
+        if (node >= j.nodes) break;
         uint32_t *dst = reinterpret_cast<uint32_t *>(
-            p.out + ((int64_t)(seq.first + node) * p.q_heads + h * p.group + (row & (p.group - 1))) * HEAD_DIM + lane * V);
+            p.out + ((int64_t)(j.first + node) * p.q_heads + h * p.group + (row & (p.group - 1))) * HEAD_DIM + lane * V);
 #pragma unroll
         for (int e = 0; e < V; e += 2)
             dst[e / 2] = M[r] == -INFINITY ? pack_bf16x2(none[r], none[r]) : pack_bf16x2(acc[r][e] / den[r], acc[r][e + 1] / den[r]);
