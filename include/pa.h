@@ -593,6 +593,7 @@ int pa_tree_masks(int32_t *masks, int32_t *positions, const int32_t *parents, co
  *                  this many tokens or more (a multiple of 128; no cut when
  *                  max_seq_len is at most twice that), -1 = no cut: results
  *                  then do not depend on the rest of the batch.
+ * scale          : finite and not negative (else PA_ERR_INVALID_ARG)
  * workspace      : pa_decode_tree_workspace_size(...) bytes, 16-byte aligned
  *                  (may be NULL if that is 0); no initialisation needed.
  * A block id outside [0, num_blocks) sets PA_FLAG_BAD_BLOCK and its tokens

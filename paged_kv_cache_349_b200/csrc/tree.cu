@@ -163,6 +163,7 @@ int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tre
         pa::bad_rows(v_tree, v_stride, num_kv_heads, head_dim))
         return PA_ERR_INVALID_ARG;
     if (partition_tokens > 0 && partition_tokens % 128) return PA_ERR_INVALID_ARG;
+    if (!(scale >= 0.f && scale < 3.0e38f)) return PA_ERR_INVALID_ARG;
     if (batch > 65535 || num_q_heads > 65535) return PA_ERR_UNSUPPORTED;
     const uint64_t rows = (uint64_t)num_blocks * (uint64_t)num_kv_heads * (uint64_t)block_size;
     if (rows >= (1ull << 31)) return PA_ERR_UNSUPPORTED;  // TMA row coordinate is int32

@@ -221,9 +221,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// mbar_wait_bounded without reading the clock when the phase is already there.
+// mbar_wait_bounded without reading the clock when the phase is already there, and with the loop kept in one
+// place: the kernel waits in some twenty of them, and its warps run different parts of it at the same time, so
+// that instruction fetches are what they stall on most.
+__device__ __noinline__ bool tree_wait_long(uint64_t *bar, uint32_t parity, int32_t *flag) {
+    return mbar_wait_bounded(bar, parity, flag);
+}
 __device__ __forceinline__ bool tree_wait(uint64_t *bar, uint32_t parity, int32_t *flag) {
-    return mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, flag);
+    return mbar_try_wait(bar, parity) || tree_wait_long(bar, parity, flag);
 }
 // Barriers kept in a ring: use n of it has its place and its parity (ring lengths are powers of two).
 template <uint32_t N>
@@ -586,11 +591,18 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             }
         };
         // Tiles are drawn ahead of their loads, so that table entries are there when they are needed.
-        Tile t0 = next_tile(), t1 = next_tile(), older = t0;
+        Tile t0{}, t1{}, older{};
         uint32_t n = UINT32_MAX;  // tiles of this CTA, once known
-        for (uint32_t t = 0;; ++t) {
-            if (n == UINT32_MAX) {
-                if (!take_slot(k_item(t))) break;
+#pragma unroll 1
+        for (uint32_t t = UINT32_MAX;; ++t) {  // one turn before tile 0
+            older = t0;
+            t0 = t1;
+            t1 = next_tile();
+            if (t == UINT32_MAX) continue;
+            // Everything that does not need the slot comes before the wait for it: in steady state the loads
+            // wait for slots, and what lies between a free slot and its copy is lost.
+            const bool mine = n == UINT32_MAX;  // there is a description to publish
+            if (mine) {
                 const uint32_t holes = __ballot_sync(0xffffffffu, t0.mine && box == 0 && (t0.id < 0 || t0.id >= p.num_blocks));
                 if (holes) {
                     if (lane == 0) raise_flag(p.err_flag, PA_FLAG_BAD_BLOCK);
@@ -600,15 +612,9 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 const bool free = t < C::kMetas || ring_wait<C::kMetas>(meta_free, t - C::kMetas, p.err_flag);
                 if (!__all_sync(0xffffffffu, free)) break;
                 if (lane == 0) {
-                    TileMeta &d = meta[mt];
-                    d.flags = t0.flags;
-                    d.start = t0.start;
-                    d.valid = t0.valid;
-                    d.dest = t0.dest;
-                    d.first = t0.first;
-                    d.nodes = t0.nodes;
-                    d.node0 = t0.node0;
-                    d.h = t0.h;
+                    int4 *d = reinterpret_cast<int4 *>(meta + mt);
+                    d[0] = make_int4(t0.flags, t0.start, t0.valid, t0.dest);
+                    d[1] = make_int4(t0.first, t0.nodes, t0.node0, t0.h);
                 }
                 if (!(t0.flags & (kPlain | kEnd)) && lane < 4) {
                     uint32_t bits = low_bits(t0.valid - 32 * lane);
@@ -621,20 +627,18 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(meta_full + mt);
-                if (t0.flags & kEnd)
+                if (t0.flags & kEnd) {
                     n = t;
-                else
+                } else {
+                    if (!take_slot(k_item(t))) break;
                     load(t0, true, k_item(t));
+                }
             }
-            const uint32_t u = t - (kBufs - 1);  // the tile whose V comes next
             if (t >= kBufs - 1) {
-                if (u >= n) break;
-                if (!take_slot(v_item(u))) break;
+                const uint32_t u = t - (kBufs - 1);  // the tile whose V comes next
+                if (u >= n || !take_slot(v_item(u))) break;
                 load(kBufs == 1 ? t0 : older, false, v_item(u));
             }
-            older = t0;
-            t0 = t1;
-            t1 = next_tile();
         }
         // If this CTA begins at the first cut inside a unit: how many pieces that unit has.
         if (p.part_o && lane == 0) {
@@ -744,9 +748,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         const int r = threadIdx.x & (kTileM - 1);
         const uint32_t base = tmem + s * C::kStreamCols + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t o_addr = base + 128;
-        // a negative scale turns the order of the scores around; a scale of 0 must not meet -inf
-        const bool flip = p.scale_log2 < 0.f;
-        const float c = p.scale_log2 == 0.f ? 1e-30f : fabsf(p.scale_log2);
+        const float c = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;  // a scale of 0 must not meet -inf
         const float rise = kMaxRise / c;
 
         // One thread of each stream loads its queries: the first piece's at once, the next one's when the
@@ -831,10 +833,6 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
 #pragma unroll
             for (int q = 0; q < kTileN / 32; ++q) tmem_ld32(s_addr + 32 * q, x + 32 * q);
             tmem_wait_ld();
-            if (flip) {
-#pragma unroll
-                for (int i = 0; i < kTileN; ++i) x[i] = -x[i];
-            }
             if (!(flags & kPlain)) {
 #pragma unroll
                 for (int i = 0; i < kTileN; ++i) x[i] = (see[i >> 5] >> (i & 31)) & 1u ? x[i] : -INFINITY;
@@ -852,7 +850,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                     ok = tree_wait(pv_done + s, (g - 1) & 1, p.err_flag);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < HEAD_DIM / 16; ++q) {
                         uint32_t w[16];
                         tmem_ld16(o_addr + 16 * q, w);
@@ -977,44 +975,46 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             else if (m == -INFINITY && seen)
                 l = NAN;
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            // 16 columns at a time: 64 bytes of a partial state, half of that of a whole unit's bf16 rows
+            uint4 v[4];
 #pragma unroll 1
-            for (int q = 0; q < HEAD_DIM / 32; ++q) {
-                float o[32];
+            for (int q = 0; q < HEAD_DIM / 16; ++q) {
+                uint32_t o[16];
                 __syncwarp();
-                tmem_ld32(o_addr + 32 * q, o);
+                tmem_ld16(o_addr + 16 * q, o);
                 tmem_wait_ld();
                 if (live && dirty) {  // the values that were kept out of the product
+#pragma unroll 1
                     for (int k = 0; k < nodes; ++k) {
                         const bool sees = p.masks ? (__ldg(p.masks + (int64_t)(first + node) * p.words + (k >> 5)) >> (k & 31)) & 1
                                                   : k <= node;
                         if (!sees) continue;
-                        const uint16_t *src = p.v_tree + (int64_t)(first + k) * p.v_stride + h * HEAD_DIM + 32 * q;
+                        const uint16_t *src = p.v_tree + (int64_t)(first + k) * p.v_stride + h * HEAD_DIM + 16 * q;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             const uint32_t bits = (uint32_t)src[i] << 16;
-                            if ((bits & 0x7f800000u) == 0x7f800000u) o[i] += __uint_as_float(bits);
+                            if ((bits & 0x7f800000u) == 0x7f800000u) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(bits));
                         }
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
-                uint4 v[4];
+                for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
                 if (whole) {
+                    uint32_t b[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-                    store64(64 * q, v);
+                    for (int i = 0; i < 8; ++i) b[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                    v[2] = make_uint4(b[0], b[1], b[2], b[3]);
+                    v[3] = make_uint4(b[4], b[5], b[6], b[7]);
+                    if (!(q & 1)) {
+                        v[0] = v[2];
+                        v[1] = v[3];
+                        continue;
+                    }
                 } else {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = make_uint4(__float_as_uint(o[16 * half + 4 * i]), __float_as_uint(o[16 * half + 4 * i + 1]),
-                                              __float_as_uint(o[16 * half + 4 * i + 2]), __float_as_uint(o[16 * half + 4 * i + 3]));
-                        store64(128 * q + 64 * half, v);
-                    }
+                    for (int i = 0; i < 4; ++i) v[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
+                store64(whole ? 32 * (q - 1) : 64 * q, v);
             }
             if (live && !whole)
                 *reinterpret_cast<float2 *>(p.part_ml + (state + r) * 2) = make_float2(m == -INFINITY ? m : m * c, l);

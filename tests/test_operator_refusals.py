@@ -42,6 +42,8 @@ def test_decode_tree_refusals():
         assert call(**bad) == INVALID, bad
     for bad in (dict(d=96), dict(bs=12), dict(Hq=6, Hkv=4), dict(Hq=32, Hkv=2), dict(NB=1 << 30), dict(B=70000)):
         assert call(**bad) == UNSUPPORTED, bad
+    for bad in (-0.1, math.inf, math.nan):
+        assert call(scale=bad) == INVALID, bad
     assert call(pt=128, maxlen=257) == INVALID  # needs a workspace
     assert call(pt=64) == INVALID and call(pt=16) == INVALID  # partitions are multiples of 128 tokens
 
