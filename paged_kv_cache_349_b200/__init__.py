@@ -374,50 +374,90 @@ class DecodeStepHost:
 
 # ---------------------------------------------------------------------------
 # Drafting and verifying several tokens in one step
+#
+# These calls are short (several take under 10 us on the GPU), so their argument checks read each attribute
+# of a tensor once and pass plain integers to the library.
 # ---------------------------------------------------------------------------
 
-def _here(t, dtype, name):
-    """Pointer of a contiguous tensor on the current device (None passes as NULL)."""
+class _Env:
+    """What the checks need of torch, looked up once."""
+
+    def __init__(self):
+        torch = _torch()
+        self.Tensor, self.bf16, self.i32, self.u8, self.f64 = (torch.Tensor, torch.bfloat16, torch.int32, torch.uint8,
+                                                               torch.float64)
+        self.device = torch._C._cuda_getDevice
+        self.stream = torch._C._cuda_getCurrentRawStream
+
+
+_env_cache = None
+
+
+def _env() -> _Env:
+    global _env_cache
+    if _env_cache is None:
+        _env_cache = _Env()
+    return _env_cache
+
+
+def _refuse(t, dtype, name, dev, contiguous=True):
+    if not isinstance(t, _env().Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if contiguous:
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"the heads of a row of {name} must be contiguous")
+
+
+def _at(t, dtype, name, dev):
+    """Address of a contiguous tensor of the current device ``dev`` (None passes as NULL)."""
     if t is None:
         return None
-    p = _dev(t, dtype, name)
-    if t.device.index != _torch().cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return p
+    if not (isinstance(t, _env_cache.Tensor) and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev):
+        _refuse(t, dtype, name, dev)
+    return t.data_ptr()
 
 
-def _rows(t, heads, name):
-    """Pointer and row stride (elements) of bf16 rows [T, heads, d] whose heads are contiguous within a row."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
+def _rows_at(t, name, dev):
+    """Address, row stride in elements and head count of bf16 rows [T, H, d] whose heads are contiguous in a row."""
+    env = _env_cache
+    if not (isinstance(t, env.Tensor) and t.dtype is env.bf16 and t.get_device() == dev):
+        _refuse(t, env.bf16, name, dev)
     n, h, d = t.shape
-    if h != heads:
-        raise ValueError(f"{name} must hold {heads} heads, got {h}")
     row, head, one = t.stride()
-    if t.numel() and ((one != 1 and d > 1) or (head != d and h > 1)):
-        raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), (row if n > 1 else h * d)
+    if (one != 1 and d > 1) or (head != d and h > 1):
+        if t.numel():
+            _refuse(t, env.bf16, name, dev, contiguous=False)
+    return t.data_ptr(), (row if n > 1 else h * d), h
+
+
+def _call(fn, where, stream, dev, *args):
+    if stream is None:
+        raw = _env_cache.stream(dev)
+    else:
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+    status = fn(*args, raw)
+    if status:
+        raise PaError(status, where)
 
 
 def pa_tree_masks(masks, positions, parents, cu_nodes, seq_lens, *, max_nodes: int, err_flag=None,
                   stream=None) -> None:
     """Ancestor masks (int32 [T, ceil(max_nodes/32)]) and positions (int32 [T], may be None) of drafted trees from
     ``parents`` int32 [T] (-1: follows the cache), ``cu_nodes`` int32 [B+1] and the cached lengths int32 [B]."""
-    torch = _torch()
-    T, B, i32 = parents.numel(), seq_lens.numel(), torch.int32
-    if cu_nodes.numel() != B + 1 or tuple(masks.shape) != (T, -(-max_nodes // 32)):
+    env = _env()
+    i32, dev = env.i32, env.device()
+    at = (_at(masks, i32, "masks", dev), _at(positions, i32, "positions", dev), _at(parents, i32, "parents", dev),
+          _at(cu_nodes, i32, "cu_nodes", dev), _at(seq_lens, i32, "seq_lens", dev))
+    T, B = parents.numel(), seq_lens.numel()
+    if cu_nodes.numel() != B + 1 or masks.shape != (T, -(-max_nodes // 32)):
         raise ValueError("cu_nodes must be [B+1] and masks [T, ceil(max_nodes/32)]")
     if positions is not None and positions.numel() != T:
         raise ValueError("positions must have one entry per row")
-    _check(lib.pa_tree_masks(_here(masks, i32, "masks"), _here(positions, i32, "positions"),
-                             _here(parents, i32, "parents"), _here(cu_nodes, i32, "cu_nodes"),
-                             _here(seq_lens, i32, "seq_lens"), B, T, int(max_nodes), _opt_flag(err_flag),
-                             _stream(stream)), "pa_tree_masks")
+    _call(lib.pa_tree_masks, "pa_tree_masks", stream, dev, *at, B, T, max_nodes, _at(err_flag, i32, "err_flag", dev))
 
 
 def pa_decode_tree_workspace_size(batch, num_rows, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
@@ -434,29 +474,32 @@ def pa_decode_tree(out, q, k_tree, v_tree, k_cache, v_cache, block_tables, seq_l
 
     Rows of sequence b are [cu_nodes[b], cu_nodes[b+1]); q, k_tree and v_tree may be parts of one projection's output.
     """
-    torch = _torch()
-    i32, bf16 = torch.int32, torch.bfloat16
+    env = _env()
+    i32, bf16, dev = env.i32, env.bf16, env.device()
+    q_at, q_row, _ = _rows_at(q, "q", dev)
+    k_at, k_row, _ = _rows_at(k_tree, "k_tree", dev)
+    v_at, v_row, _ = _rows_at(v_tree, "v_tree", dev)
+    pools = _at(k_cache, bf16, "k_cache", dev), _at(v_cache, bf16, "v_cache", dev)
     T, Hq, d = q.shape
     NB, Hkv, bs, d2 = k_cache.shape
     B = seq_lens.numel()
     if d2 != d or out.shape != q.shape or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch")
-    if tuple(k_tree.shape) != (T, Hkv, d) or v_tree.shape != k_tree.shape:
+    if k_tree.shape != (T, Hkv, d) or v_tree.shape != (T, Hkv, d):
         raise ValueError("k_tree/v_tree must be [T, Hkv, d]")
     if block_tables.dim() != 2 or block_tables.shape[0] != B or cu_nodes.numel() != B + 1:
         raise ValueError("block_tables must be [B, max_blocks], seq_lens [B] and cu_nodes [B+1]")
-    if masks is not None and tuple(masks.shape) != (T, -(-max_nodes // 32)):
+    if masks is not None and masks.shape != (T, -(-max_nodes // 32)):
         raise ValueError("masks must be [T, ceil(max_nodes/32)]")
-    ws_ptr, ws_bytes = None, 0
+    ws_at, ws_bytes = None, 0
     if workspace is not None:
-        ws_ptr = _here(workspace, workspace.dtype, "workspace")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib.pa_decode_tree(
-        _here(out, bf16, "out"), *_rows(q, Hq, "q"), *_rows(k_tree, Hkv, "k_tree"), *_rows(v_tree, Hkv, "v_tree"), T,
-        _here(k_cache, bf16, "k_cache"), _here(v_cache, bf16, "v_cache"), _here(block_tables, i32, "block_tables"),
-        block_tables.shape[1], _here(seq_lens, i32, "seq_lens"), _here(cu_nodes, i32, "cu_nodes"),
-        _here(masks, i32, "masks"), B, int(max_seq_len), int(max_nodes), Hq, Hkv, d, bs, NB, float(scale),
-        int(partition_tokens), ws_ptr, ws_bytes, _opt_flag(err_flag), _stream(stream)), "pa_decode_tree")
+        ws_at = _at(workspace, workspace.dtype, "workspace", dev)
+        ws_bytes = workspace.nbytes
+    _call(lib.pa_decode_tree, "pa_decode_tree", stream, dev, _at(out, bf16, "out", dev), q_at, q_row, k_at, k_row, v_at,
+          v_row, T, *pools, _at(block_tables, i32, "block_tables", dev), block_tables.shape[1],
+          _at(seq_lens, i32, "seq_lens", dev), _at(cu_nodes, i32, "cu_nodes", dev), _at(masks, i32, "masks", dev), B,
+          max_seq_len, max_nodes, Hq, Hkv, d, bs, NB, scale, partition_tokens, ws_at, ws_bytes,
+          _at(err_flag, i32, "err_flag", dev))
 
 
 def pa_extend_tables(block_tables, seq_lens, add_lens, free_blocks, free_cursor, *, num_blocks: int, block_size: int,
@@ -468,28 +511,34 @@ def pa_extend_tables(block_tables, seq_lens, add_lens, free_blocks, free_cursor,
     ``seq_lens_out`` and ``cursor_out`` default to updating ``seq_lens`` and ``free_cursor`` in place.  With
     ``cu_rows`` int32 [B+1] and ``path`` int32 [B, max_path] the slots go to the accepted rows of drafted trees.
     """
-    i32 = _torch().int32
+    env = _env()
+    i32, dev = env.i32, env.device()
+    lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    cur_out = free_cursor if cursor_out is None else cursor_out
+    tables_at, lens_at = _at(block_tables, i32, "block_tables", dev), _at(seq_lens, i32, "seq_lens", dev)
+    add_at, free_at = _at(add_lens, i32, "add_lens", dev), _at(free_blocks, i32, "free_blocks", dev)
+    cursor_at, cu_at = _at(free_cursor, i32, "free_cursor", dev), _at(cu_tokens, i32, "cu_tokens", dev)
+    slots_at, positions_at = _at(slot_mapping, i32, "slot_mapping", dev), _at(positions, i32, "positions", dev)
     B, T = seq_lens.numel(), slot_mapping.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != B or add_lens.numel() != B or cu_tokens.numel() != B + 1:
         raise ValueError("block_tables must be [B, max_blocks], add_lens [B] and cu_tokens [B+1]")
     if positions is not None and positions.numel() != T:
         raise ValueError("positions must have one entry per row")
-    if (cu_rows is None) != (path is None):
-        raise ValueError("pass both cu_rows and path, or neither")
-    if path is not None and (path.dim() != 2 or path.shape[0] != B or cu_rows.numel() != B + 1):
-        raise ValueError("cu_rows must be [B+1] and path [B, max_path]")
-    lens_out = seq_lens if seq_lens_out is None else seq_lens_out
-    cur_out = free_cursor if cursor_out is None else cursor_out
+    rows_at = path_at = None
+    max_path = 0
+    if cu_rows is not None or path is not None:
+        if cu_rows is None or path is None:
+            raise ValueError("pass both cu_rows and path, or neither")
+        rows_at, path_at = _at(cu_rows, i32, "cu_rows", dev), _at(path, i32, "path", dev)
+        if path.dim() != 2 or path.shape[0] != B or cu_rows.numel() != B + 1:
+            raise ValueError("cu_rows must be [B+1] and path [B, max_path]")
+        max_path = path.shape[1]
     if lens_out.numel() != B or free_cursor.numel() != 1 or cur_out.numel() != 1:
         raise ValueError("seq_lens_out must be [B], the cursors one entry")
-    _check(lib.pa_extend_tables(
-        _here(block_tables, i32, "block_tables"), block_tables.shape[1], _here(seq_lens, i32, "seq_lens"),
-        _here(add_lens, i32, "add_lens"), _here(lens_out, i32, "seq_lens_out"), B, int(block_size), int(num_blocks),
-        _here(free_blocks, i32, "free_blocks"), free_blocks.numel(), _here(free_cursor, i32, "free_cursor"),
-        _here(cur_out, i32, "cursor_out"), _here(slot_mapping, i32, "slot_mapping"),
-        _here(positions, i32, "positions"), _here(cu_tokens, i32, "cu_tokens"), T, _here(cu_rows, i32, "cu_rows"),
-        _here(path, i32, "path"), 0 if path is None else path.shape[1], _opt_flag(err_flag), _stream(stream)),
-        "pa_extend_tables")
+    _call(lib.pa_extend_tables, "pa_extend_tables", stream, dev, tables_at, block_tables.shape[1], lens_at, add_at,
+          _at(lens_out, i32, "seq_lens_out", dev), B, block_size, num_blocks, free_at, free_blocks.numel(), cursor_at,
+          _at(cur_out, i32, "cursor_out", dev), slots_at, positions_at, cu_at, T, rows_at, path_at, max_path,
+          _at(err_flag, i32, "err_flag", dev))
 
 
 # ---------------------------------------------------------------------------
@@ -518,69 +567,69 @@ def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "
     return turns, gain.value
 
 
-def _rope_args(q, q_out, positions, turns, T, d):
-    torch = _torch()
-    if (q is None) != (q_out is None):
-        raise ValueError("pass both q and q_out, or neither")
-    if positions.numel() != T:
-        raise ValueError("positions must have one entry per token")
-    head = (None, 0, None, 0, 0)
-    if q is not None:
-        Hq = q.shape[1]
-        if q.shape != q_out.shape or q.shape[0] != T or q.shape[2] != d:
-            raise ValueError("q and q_out must be [T, Hq, d]")
-        head = (*_rows(q, Hq, "q"), *_rows(q_out, Hq, "q_out"), Hq)
-    tail = (_here(positions, torch.int32, "positions"), _here(turns, torch.float64, "turns"), 2 * turns.numel())
-    return head, tail
+def _rope_pair(x, x_out, name, T, d, dev):
+    """Addresses, strides and head count of rows and of what they become; all 0 when both are None."""
+    if x is None and x_out is None:
+        return None, 0, None, 0, 0
+    if x is None or x_out is None:
+        raise ValueError(f"pass both {name} and {name}_out, or neither")
+    at, row, heads = _rows_at(x, name, dev)
+    out_at, out_row, _ = _rows_at(x_out, name + "_out", dev)
+    if x.shape != x_out.shape or x.shape[0] != T or x.shape[2] != d:
+        raise ValueError(f"{name} and {name}_out must be [T, heads, d]")
+    return at, row, out_at, out_row, heads
 
 
 def pa_rope(q, q_out, k, k_out, positions, turns, *, interleaved: bool = False, gain: float = 1.0,
             stream=None) -> None:
     """Rotate q [T, Hq, d] into q_out and k [T, Hkv, d] into k_out (each pair may be None, or one tensor twice)."""
-    if (k is None) != (k_out is None):
-        raise ValueError("pass both k and k_out, or neither")
+    env = _env()
+    dev = env.device()
     some = q if q is not None else k
     if some is None:
         raise ValueError("nothing to rotate")
     T, _, d = some.shape
-    head, tail = _rope_args(q, q_out, positions, turns, T, d)
-    keys = (None, 0, None, 0, 0)
-    if k is not None:
-        if k.shape != k_out.shape or k.shape[0] != T or k.shape[2] != d:
-            raise ValueError("k and k_out must be [T, Hkv, d]")
-        keys = (*_rows(k, k.shape[1], "k"), *_rows(k_out, k.shape[1], "k_out"), k.shape[1])
-    _check(lib.pa_rope(*head, *keys, *tail, int(bool(interleaved)), float(gain), T, d, _stream(stream)), "pa_rope")
+    positions_at, turns_at = _at(positions, env.i32, "positions", dev), _at(turns, env.f64, "turns", dev)
+    if positions.numel() != T:
+        raise ValueError("positions must have one entry per token")
+    _call(lib.pa_rope, "pa_rope", stream, dev, *_rope_pair(q, q_out, "q", T, d, dev),
+          *_rope_pair(k, k_out, "k", T, d, dev), positions_at, turns_at, 2 * turns.numel(), interleaved, gain, T, d)
 
 
-def _rope_and_cache(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, pool_dtype):
-    T, Hkv, d = k.shape
+def _rope_and_cache(fn, where, stream, q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, pool_dtype,
+                    interleaved, gain, scales, err_flag):
+    env = _env_cache
+    i32, dev = env.i32, env.device()
+    k_at, k_row, Hkv = _rows_at(k, "k", dev)
+    v_at, v_row, _ = _rows_at(v, "v", dev)
+    pools = _at(k_cache, pool_dtype, "k_cache", dev), _at(v_cache, pool_dtype, "v_cache", dev)
+    slots_at, positions_at = _at(slot_mapping, i32, "slot_mapping", dev), _at(positions, i32, "positions", dev)
+    turns_at = _at(turns, env.f64, "turns", dev)
+    T, _, d = k.shape
     NB, Hkv2, bs, d2 = k_cache.shape
-    if (Hkv2, d2) != (Hkv, d) or v.shape != k.shape or v_cache.shape != k_cache.shape:
+    if Hkv2 != Hkv or d2 != d or v.shape != k.shape or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch")
-    if slot_mapping.numel() != T:
-        raise ValueError("slot_mapping must have one entry per token")
-    head, tail = _rope_args(q, q_out, positions, turns, T, d)
-    return (*head, *_rows(k, Hkv, "k"), *_rows(v, Hkv, "v"), Hkv, _here(k_cache, pool_dtype, "k_cache"),
-            _here(v_cache, pool_dtype, "v_cache"), _here(slot_mapping, _torch().int32, "slot_mapping"), NB, bs, *tail)
+    if slot_mapping.numel() != T or positions.numel() != T:
+        raise ValueError("slot_mapping and positions must have one entry per token")
+    _call(fn, where, stream, dev, *_rope_pair(q, q_out, "q", T, d, dev), k_at, k_row, v_at, v_row, Hkv, *pools, slots_at,
+          NB, bs, positions_at, turns_at, 2 * turns.numel(), interleaved, gain, T, d, *scales,
+          _at(err_flag, i32, "err_flag", dev))
 
 
 def pa_rope_and_cache(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, *, interleaved: bool = False,
                       gain: float = 1.0, err_flag=None, stream=None) -> None:
     """Rotate q [T, Hq, d] into q_out (both may be None) and write the rotated k and v [T, Hkv, d] into the bf16 pools
     at slot_mapping [T], in one launch."""
-    args = _rope_and_cache(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, _torch().bfloat16)
-    _check(lib.pa_rope_and_cache(*args, int(bool(interleaved)), float(gain), k.shape[0], k.shape[2],
-                                 _opt_flag(err_flag), _stream(stream)), "pa_rope_and_cache")
+    _rope_and_cache(lib.pa_rope_and_cache, "pa_rope_and_cache", stream, q, q_out, k, v, k_cache, v_cache, slot_mapping,
+                    positions, turns, _env().bf16, interleaved, gain, (), err_flag)
 
 
 def pa_rope_and_cache_fp8(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, *, k_scale: float,
                           v_scale: float, interleaved: bool = False, gain: float = 1.0, err_flag=None,
                           stream=None) -> None:
     """pa_rope_and_cache over uint8 E4M3 pools: the rotated k and v are quantised as they are written."""
-    args = _rope_and_cache(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, turns, _torch().uint8)
-    _check(lib.pa_rope_and_cache_fp8(*args, int(bool(interleaved)), float(gain), k.shape[0], k.shape[2],
-                                     float(k_scale), float(v_scale), _opt_flag(err_flag), _stream(stream)),
-           "pa_rope_and_cache_fp8")
+    _rope_and_cache(lib.pa_rope_and_cache_fp8, "pa_rope_and_cache_fp8", stream, q, q_out, k, v, k_cache, v_cache,
+                    slot_mapping, positions, turns, _env().u8, interleaved, gain, (k_scale, v_scale), err_flag)
 
 
 # ---------------------------------------------------------------------------
