@@ -8,8 +8,11 @@
 //
 // Bound: HBM.  Every q, k and v value is read once and written once; the angles
 // are computed once for each token and shared by all heads through shared
-// memory.  A CTA takes a few whole tokens, so that each thread has several
-// 16-byte loads in flight while the angles are being computed.
+// memory.  A thread keeps one place in the row (a head, and 16 values of it)
+// for all tokens of its CTA, so that the loop over tokens has no index
+// arithmetic; the loads of all its tokens are issued before the angles are
+// computed.  8192 tokens of 32 + 8 heads take 35 us, 5.7 TB/s (a division for each
+// 16 values: 55 us).
 #include <math.h>
 
 #include "pa_common.cuh"
@@ -17,9 +20,11 @@
 namespace pa {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 2;       // items whose loads a thread issues together
-constexpr int kRopeMaxTokens = 16;   // tokens of one CTA
+// Threads of a CTA at most, and its tokens where there are enough to fill the GPU with such CTAs.  Measured
+// (8192 tokens of 32 + 8 heads, bf16 pools | 3001 tokens of 40 + 40 heads, fp8 pools): 35.1 | 28.2 us;
+// with 512 threads and 4 tokens 53.2 | 38.8, with 256 and 4 35.3 | 29.7, with 128 and 5 38.0 | 29.4.
+constexpr int kRopeThreads = 128;
+constexpr int kRopeTokens = 3;
 
 struct RopeParams {
     const uint16_t *q, *k, *v;
@@ -29,23 +34,9 @@ struct RopeParams {
     const double *turns;
     int32_t *err_flag;
     int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride, num_slots;
-    int num_tokens, q_heads, kv_heads, rotary, block_size, tokens_per_cta;
+    int num_tokens, q_heads, kv_heads, rotary, block_size;
     float gain, k_inv_scale, v_inv_scale;
 };
-
-// An item is 16 values of one head: for a rotated item the 8 pairs 8i .. 8i+7,
-// else 16 values that pass through.  Its two 16-byte vectors start at these
-// values of the head.
-template <bool INTERLEAVED>
-__device__ __forceinline__ void item_offsets(int i, int rotary, int &a, int &b) {
-    if (!INTERLEAVED && 16 * i < rotary) {
-        a = 8 * i;
-        b = rotary / 2 + 8 * i;
-    } else {
-        a = 16 * i;
-        b = a + 8;
-    }
-}
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -71,145 +62,137 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float inv_scale)
     return make_uint2(out[0], out[1]);
 }
 
+// A place is 16 values of one head in two vectors of 8: for a rotated one the pairs 8i .. 8i+7 (values 8i.. and
+// rotary / 2 + 8i.. of the head, or 16i.. and 16i + 8.. where pairs are interleaved), else 16 that pass through.
 // CACHE: k and v go to the pools (FP8: as E4M3 codes); else the rotated k goes to k_out.
-template <int HEAD_DIM, bool INTERLEAVED, bool CACHE, bool FP8>
+template <int HEAD_DIM, bool INTERLEAVED, bool CACHE, bool FP8, int TOKENS>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-    constexpr int kItems = HEAD_DIM / 16;  // items of one head
-    // cos and sin of pairs 8i + 2s, 8i + 2s + 1 of token t at [t][s][i]: the items of a
-    // head read neighbouring 16-byte words
-    __shared__ float4 s_cs[kRopeMaxTokens * 4 * kItems];
-    const int t0 = blockIdx.x * p.tokens_per_cta;
-    const int tokens = min(p.tokens_per_cta, p.num_tokens - t0);
-    const int heads = p.q_heads + p.kv_heads * (CACHE ? 2 : 1);
-    const int total = tokens * heads * kItems;
-    const int pairs = p.rotary / 2;
+    constexpr int kPlaces = HEAD_DIM / 16;  // of one head
+    // cos and sin of pairs 8i + 2s, 8i + 2s + 1 of token t at [t][s][i]: the places of a head read
+    // neighbouring 16-byte words
+    __shared__ float4 s_cs[TOKENS * 4 * kPlaces];
+    __shared__ int64_t s_row[TOKENS];  // pool offset of the token's row of head 0, or -1
+    const int t0 = blockIdx.x * TOKENS;
+    const int tokens = min(TOKENS, p.num_tokens - t0);
+    const int places = (p.q_heads + p.kv_heads * (CACHE ? 2 : 1)) * kPlaces;
 
-    struct Item {
-        uint4 lo, hi;
-        int t, head, i;
-    };
-    auto load = [&](int x, Item &it) {
-        it.i = x % kItems;
-        const int th = x / kItems;
-        it.t = th / heads;
-        it.head = th - it.t * heads;
-        const int64_t t = t0 + it.t;
-        const uint16_t *src;
-        if (it.head < p.q_heads)
-            src = p.q + t * p.q_stride + it.head * HEAD_DIM;
-        else if (it.head < p.q_heads + p.kv_heads)
-            src = p.k + t * p.k_stride + (it.head - p.q_heads) * HEAD_DIM;
-        else
-            src = p.v + t * p.v_stride + (it.head - p.q_heads - p.kv_heads) * HEAD_DIM;
-        int a, b;
-        item_offsets<INTERLEAVED>(it.i, p.rotary, a, b);
-        if (CACHE && it.head >= p.q_heads + p.kv_heads) a = 16 * it.i, b = a + 8;  // v passes through
-        it.lo = *reinterpret_cast<const uint4 *>(src + a);
-        it.hi = *reinterpret_cast<const uint4 *>(src + b);
-    };
-    auto finish = [&](const Item &it) {
-        const bool is_q = it.head < p.q_heads;
-        const bool is_v = CACHE && it.head >= p.q_heads + p.kv_heads;
-        const int64_t t = t0 + it.t;
-        int64_t row = 0;  // pool row of a k or v item
-        if (CACHE && !is_q) {
-            const int64_t slot = __ldg(p.slots + t);
-            if (slot == -1) return;
-            if (slot < 0 || slot >= p.num_slots) {
-                if (it.i == 0 && it.head == p.q_heads) raise_flag(p.err_flag, PA_FLAG_BAD_SLOT);
-                return;
-            }
-            const int h = it.head - p.q_heads - (is_v ? p.kv_heads : 0);
-            const int64_t blk = slot / p.block_size;
-            row = ((blk * p.kv_heads + h) * p.block_size + (slot - blk * p.block_size)) * HEAD_DIM;
-        }
-        int a, b;
-        item_offsets<INTERLEAVED>(it.i, p.rotary, a, b);
-        float x[8], y[8];
-        unpack8(it.lo, x);
-        unpack8(it.hi, y);
-        const bool turn = !is_v && 16 * it.i < p.rotary;
-        if (is_v) a = 16 * it.i, b = a + 8;
-        if (turn) {
+    for (int x0 = 0; x0 < places; x0 += blockDim.x) {
+        const int x = x0 + threadIdx.x;
+        const int i = x % kPlaces, head = x / kPlaces;
+        const bool is_q = head < p.q_heads, is_v = CACHE && head >= p.q_heads + p.kv_heads;
+        const int h = is_q ? head : head - p.q_heads - (is_v ? p.kv_heads : 0);
+        const bool turn = !is_v && 16 * i < p.rotary;
+        const int a = turn && !INTERLEAVED ? 8 * i : 16 * i;
+        const int b = turn && !INTERLEAVED ? p.rotary / 2 + 8 * i : 16 * i + 8;
+        uint4 lo[TOKENS], hi[TOKENS];
+        if (x < places) {
+            const int64_t stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
+            const uint16_t *src = (is_q ? p.q : is_v ? p.v : p.k) + t0 * stride + h * HEAD_DIM;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const float4 cs = s_cs[(it.t * 4 + s) * kItems + it.i];
-                if (INTERLEAVED) {  // pairs (2e, 2e + 1): 0..3 in x, 4..7 in y
-                    float(&w)[8] = s < 2 ? x : y;
-                    const int e = 4 * (s & 1);
-                    const float a0 = w[e], b0 = w[e + 1], a1 = w[e + 2], b1 = w[e + 3];
-                    w[e] = a0 * cs.x - b0 * cs.y;
-                    w[e + 1] = b0 * cs.x + a0 * cs.y;
-                    w[e + 2] = a1 * cs.z - b1 * cs.w;
-                    w[e + 3] = b1 * cs.z + a1 * cs.w;
-                } else {
-                    const int e = 2 * s;
-                    const float a0 = x[e], b0 = y[e], a1 = x[e + 1], b1 = y[e + 1];
-                    x[e] = a0 * cs.x - b0 * cs.y;
-                    y[e] = b0 * cs.x + a0 * cs.y;
-                    x[e + 1] = a1 * cs.z - b1 * cs.w;
-                    y[e + 1] = b1 * cs.z + a1 * cs.w;
+            for (int u = 0; u < TOKENS; ++u)
+                if (u < tokens) {
+                    lo[u] = *reinterpret_cast<const uint4 *>(src + u * stride + a);
+                    hi[u] = *reinterpret_cast<const uint4 *>(src + u * stride + b);
+                }
+        }
+        if (x0 == 0) {
+            const int pairs = p.rotary / 2;
+            for (int y = threadIdx.x; y < tokens * pairs; y += blockDim.x) {
+                const int u = y / pairs, j = y - u * pairs;
+                const double at = (double)__ldg(p.positions + t0 + u) * __ldg(p.turns + j);
+                float c, s;
+                sincospif((float)(2.0 * (at - rint(at))), &s, &c);
+                // pair j is half (j & 1) of word (j / 2) % 4 of place j / 8
+                float2 *dst = reinterpret_cast<float2 *>(s_cs + (u * 4 + ((j >> 1) & 3)) * kPlaces + (j >> 3)) + (j & 1);
+                *dst = make_float2(c * p.gain, s * p.gain);
+            }
+            if (CACHE && threadIdx.x < tokens) {
+                const int64_t slot = __ldg(p.slots + t0 + threadIdx.x);
+                int64_t row = -1;
+                if (slot >= 0 && slot < p.num_slots) {
+                    const int64_t blk = slot / p.block_size;
+                    row = (blk * p.kv_heads * p.block_size + (slot - blk * p.block_size)) * HEAD_DIM;
+                } else if (slot != -1) {
+                    raise_flag(p.err_flag, PA_FLAG_BAD_SLOT);
+                }
+                s_row[threadIdx.x] = row;
+            }
+            __syncthreads();
+        }
+        if (x >= places) continue;
+#pragma unroll
+        for (int u = 0; u < TOKENS; ++u) {
+            if (u >= tokens) break;
+            float v[8], w[8];
+            unpack8(lo[u], v);
+            unpack8(hi[u], w);
+            if (turn) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const float4 cs = s_cs[(u * 4 + s) * kPlaces + i];
+                    if (INTERLEAVED) {  // pairs (2e, 2e + 1): 0..3 in v, 4..7 in w
+                        float(&z)[8] = s < 2 ? v : w;
+                        const int e = 4 * (s & 1);
+                        const float a0 = z[e], b0 = z[e + 1], a1 = z[e + 2], b1 = z[e + 3];
+                        z[e] = a0 * cs.x - b0 * cs.y;
+                        z[e + 1] = b0 * cs.x + a0 * cs.y;
+                        z[e + 2] = a1 * cs.z - b1 * cs.w;
+                        z[e + 3] = b1 * cs.z + a1 * cs.w;
+                    } else {
+                        const int e = 2 * s;
+                        const float a0 = v[e], b0 = w[e], a1 = v[e + 1], b1 = w[e + 1];
+                        v[e] = a0 * cs.x - b0 * cs.y;
+                        w[e] = b0 * cs.x + a0 * cs.y;
+                        v[e + 1] = a1 * cs.z - b1 * cs.w;
+                        w[e + 1] = b1 * cs.z + a1 * cs.w;
+                    }
                 }
             }
+            if (CACHE && !is_q) {
+                int64_t row = s_row[u];
+                if (row < 0) continue;
+                row += (int64_t)h * p.block_size * HEAD_DIM;
+                if (FP8) {
+                    uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) + row;
+                    const float inv = is_v ? p.v_inv_scale : p.k_inv_scale;
+                    *reinterpret_cast<uint2 *>(dst + a) = quantise8(v, inv);
+                    *reinterpret_cast<uint2 *>(dst + b) = quantise8(w, inv);
+                    continue;
+                }
+                uint16_t *dst = static_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + row;
+                *reinterpret_cast<uint4 *>(dst + a) = turn ? pack8(v) : lo[u];
+                *reinterpret_cast<uint4 *>(dst + b) = turn ? pack8(w) : hi[u];
+                continue;
+            }
+            // what passes through keeps its bits
+            uint16_t *dst = (is_q ? p.q_out + (t0 + u) * p.q_out_stride : p.k_out + (t0 + u) * p.k_out_stride) + h * HEAD_DIM;
+            *reinterpret_cast<uint4 *>(dst + a) = turn ? pack8(v) : lo[u];
+            *reinterpret_cast<uint4 *>(dst + b) = turn ? pack8(w) : hi[u];
         }
-        if (CACHE && FP8 && !is_q) {
-            uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) + row;
-            const float inv = is_v ? p.v_inv_scale : p.k_inv_scale;
-            *reinterpret_cast<uint2 *>(dst + a) = quantise8(x, inv);
-            *reinterpret_cast<uint2 *>(dst + b) = quantise8(y, inv);
-            return;
-        }
-        uint16_t *dst;
-        if (is_q)
-            dst = p.q_out + t * p.q_out_stride + it.head * HEAD_DIM;
-        else if (CACHE)
-            dst = static_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + row;
-        else
-            dst = p.k_out + t * p.k_out_stride + (it.head - p.q_heads) * HEAD_DIM;
-        // what passes through keeps its bits
-        *reinterpret_cast<uint4 *>(dst + a) = turn ? pack8(x) : it.lo;
-        *reinterpret_cast<uint4 *>(dst + b) = turn ? pack8(y) : it.hi;
-    };
-
-    Item first[kRopeUnroll];
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-        const int x = threadIdx.x + u * kRopeThreads;
-        if (x < total) load(x, first[u]);
-    }
-    for (int x = threadIdx.x; x < tokens * pairs; x += kRopeThreads) {
-        const int t = x / pairs, i = x - t * pairs;
-        const double at = (double)__ldg(p.positions + t0 + t) * __ldg(p.turns + i);
-        float c, s;
-        sincospif((float)(2.0 * (at - rint(at))), &s, &c);
-        // pair i is half (i & 1) of word (i / 2) % 4 of item i / 8
-        float2 *dst = reinterpret_cast<float2 *>(s_cs + (t * 4 + ((i >> 1) & 3)) * kItems + (i >> 3)) + (i & 1);
-        *dst = make_float2(c * p.gain, s * p.gain);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-        const int x = threadIdx.x + u * kRopeThreads;
-        if (x < total) finish(first[u]);
-    }
-    for (int x0 = threadIdx.x + kRopeUnroll * kRopeThreads; x0 < total; x0 += kRopeUnroll * kRopeThreads) {
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u)
-            if (x0 + u * kRopeThreads < total) load(x0 + u * kRopeThreads, first[u]);
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u)
-            if (x0 + u * kRopeThreads < total) finish(first[u]);
     }
 }
 
-template <int HEAD_DIM, bool INTERLEAVED>
-void launch_rope(const RopeParams &p, bool cache, bool fp8, unsigned grid, cudaStream_t s) {
+template <int HEAD_DIM, bool INTERLEAVED, int TOKENS>
+void launch_rope_n(const RopeParams &p, bool cache, bool fp8, cudaStream_t s) {
+    // As few passes over the places of a row as kRopeThreads allow, of equal size.
+    const int places = (p.q_heads + p.kv_heads * (cache ? 2 : 1)) * (HEAD_DIM / 16);
+    const int passes = (places + kRopeThreads - 1) / kRopeThreads;
+    const int threads = ((places + passes - 1) / passes + 31) / 32 * 32;
+    const unsigned grid = (unsigned)((p.num_tokens + TOKENS - 1) / TOKENS);
     if (!cache)
-        rope_kernel<HEAD_DIM, INTERLEAVED, false, false><<<grid, kRopeThreads, 0, s>>>(p);
+        rope_kernel<HEAD_DIM, INTERLEAVED, false, false, TOKENS><<<grid, threads, 0, s>>>(p);
     else if (fp8)
-        rope_kernel<HEAD_DIM, INTERLEAVED, true, true><<<grid, kRopeThreads, 0, s>>>(p);
+        rope_kernel<HEAD_DIM, INTERLEAVED, true, true, TOKENS><<<grid, threads, 0, s>>>(p);
     else
-        rope_kernel<HEAD_DIM, INTERLEAVED, true, false><<<grid, kRopeThreads, 0, s>>>(p);
+        rope_kernel<HEAD_DIM, INTERLEAVED, true, false, TOKENS><<<grid, threads, 0, s>>>(p);
+}
+
+template <int HEAD_DIM, bool INTERLEAVED>
+void launch_rope(const RopeParams &p, bool cache, bool fp8, cudaStream_t s) {
+    if (p.num_tokens >= 4 * kRopeTokens * device_sm_count())
+        launch_rope_n<HEAD_DIM, INTERLEAVED, kRopeTokens>(p, cache, fp8, s);
+    else
+        launch_rope_n<HEAD_DIM, INTERLEAVED, 1>(p, cache, fp8, s);
 }
 
 bool bad_rows(const void *p, int64_t stride, int heads, int head_dim) {
@@ -230,19 +213,11 @@ int rope_impl(RopeParams p, int head_dim, int interleaved, bool cache, bool fp8,
                       bad_rows(p.q_out, p.q_out_stride, p.q_heads, head_dim)))
         return PA_ERR_INVALID_ARG;
     if (p.kv_heads && bad_rows(p.k, p.k_stride, p.kv_heads, head_dim)) return PA_ERR_INVALID_ARG;
-    // As many tokens for a CTA as give every thread kRopeUnroll items, as long as that leaves four
-    // CTAs for each SM: a few tokens alone are spread over as many SMs as they can fill.
-    const int per_token = heads * (head_dim / 16);
-    int tokens = (kRopeThreads * kRopeUnroll) / per_token;
-    const int spread = (p.num_tokens + 4 * device_sm_count() - 1) / (4 * device_sm_count());
-    if (tokens > spread) tokens = spread;
-    p.tokens_per_cta = tokens < 1 ? 1 : tokens > kRopeMaxTokens ? kRopeMaxTokens : tokens;
-    const unsigned grid = (unsigned)((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (head_dim == 128)
-        interleaved ? launch_rope<128, true>(p, cache, fp8, grid, s) : launch_rope<128, false>(p, cache, fp8, grid, s);
+        interleaved ? launch_rope<128, true>(p, cache, fp8, s) : launch_rope<128, false>(p, cache, fp8, s);
     else
-        interleaved ? launch_rope<64, true>(p, cache, fp8, grid, s) : launch_rope<64, false>(p, cache, fp8, grid, s);
+        interleaved ? launch_rope<64, true>(p, cache, fp8, s) : launch_rope<64, false>(p, cache, fp8, s);
     count_launch();
     return launch_status();
 }
