@@ -113,7 +113,8 @@ int launch_tree(const TreeMaps &m, const TreeParams &p, cudaStream_t stream) {
     const int st = launch_status();
     if (st != PA_OK || !p.part_o) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)(STREAMS * kTileM / kJoinRows));
+    const int rows = min(STREAMS * kTileM, p.max_nodes * p.group);  // of a unit, at most
+    cfg.gridDim = dim3((unsigned)(ctas - 1), (unsigned)((rows + kJoinRows - 1) / kJoinRows));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -975,13 +975,12 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             else if (m == -INFINITY && seen)
                 l = NAN;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            // 16 columns at a time: 64 bytes of a partial state, half of that of a whole unit's bf16 rows
-            uint4 v[4];
+            // 32 columns at a time: 128 bytes of a partial state, half of that of a whole unit's bf16 rows
 #pragma unroll 1
-            for (int q = 0; q < HEAD_DIM / 16; ++q) {
-                uint32_t o[16];
+            for (int q = 0; q < HEAD_DIM / 32; ++q) {
+                float o[32];
                 __syncwarp();
-                tmem_ld16(o_addr + 16 * q, o);
+                tmem_ld32(o_addr + 32 * q, o);
                 tmem_wait_ld();
                 if (live && dirty) {  // the values that were kept out of the product
 #pragma unroll 1
@@ -989,32 +988,33 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                         const bool sees = p.masks ? (__ldg(p.masks + (int64_t)(first + node) * p.words + (k >> 5)) >> (k & 31)) & 1
                                                   : k <= node;
                         if (!sees) continue;
-                        const uint16_t *src = p.v_tree + (int64_t)(first + k) * p.v_stride + h * HEAD_DIM + 16 * q;
+                        const uint16_t *src = p.v_tree + (int64_t)(first + k) * p.v_stride + h * HEAD_DIM + 32 * q;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 32; ++i) {
                             const uint32_t bits = (uint32_t)src[i] << 16;
-                            if ((bits & 0x7f800000u) == 0x7f800000u) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(bits));
+                            if ((bits & 0x7f800000u) == 0x7f800000u) o[i] += __uint_as_float(bits);
                         }
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+                for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
+                uint4 v[4];
                 if (whole) {
-                    uint32_t b[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) b[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-                    v[2] = make_uint4(b[0], b[1], b[2], b[3]);
-                    v[3] = make_uint4(b[4], b[5], b[6], b[7]);
-                    if (!(q & 1)) {
-                        v[0] = v[2];
-                        v[1] = v[3];
-                        continue;
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                    store64(64 * q, v);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = make_uint4(__float_as_uint(o[16 * x + 4 * i]), __float_as_uint(o[16 * x + 4 * i + 1]),
+                                              __float_as_uint(o[16 * x + 4 * i + 2]), __float_as_uint(o[16 * x + 4 * i + 3]));
+                        store64(128 * q + 64 * x, v);
+                    }
                 }
-                store64(whole ? 32 * (q - 1) : 64 * q, v);
             }
             if (live && !whole)
                 *reinterpret_cast<float2 *>(p.part_ml + (state + r) * 2) = make_float2(m == -INFINITY ? m : m * c, l);
@@ -1043,7 +1043,7 @@ constexpr int kJoinWarps = 8;
 constexpr int kJoinRows = 32;
 
 template <int HEAD_DIM, int STREAMS>
-__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) tree_join_kernel(const TreeParams p) {
     constexpr int V = HEAD_DIM / 32, R = kJoinRows / kJoinWarps;
     constexpr int kRows = STREAMS * kTileM;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
