@@ -16,26 +16,28 @@
 //    whole call and takes an equal share of all tiles, in order, so that neither
 //    the lengths nor the number of sequences leave SMs idle; a unit that is cut by
 //    a border between two CTAs leaves partial states for a second kernel.
-//  * A producer warp walks the units, dereferences the block table and stages the
-//    tiles of K and V with TMA into one ring, in the order in which they are used.
-//    It describes each tile (sequence, rows, valid tokens) in a ring of its own.
-//  * One thread issues the products.  S = Q K^T (bf16, fp32 accumulator in TMEM) and
-//    O += P V with P read from TMEM.
+//  * Two producer warps walk the units, dereference the block table and stage tiles
+//    with TMA, one those of K, one those of V, each into its own ring.  The first
+//    also describes each tile (sequence, rows, valid tokens) in a ring of its own.
+//  * One thread for each 128 rows issues the products: S = Q K^T (bf16, fp32
+//    accumulator in TMEM) and O += P V with P read from TMEM.
 //  * Four warps for each 128 rows run the softmax, a row to a thread: no shuffles.
-//    P replaces its scores in TMEM as bf16: 8 significant bits for each weight, as
-//    many as the values it multiplies have, and as the output keeps; the sum of the
-//    weights is fp32 and unrounded.
+//    P goes back to TMEM as bf16: 8 significant bits for each weight, as many as the
+//    values it multiplies have, and as the output keeps; the sum of the weights is
+//    fp32 and unrounded.
+//  * A tile is 64 tokens: a thread holds its row's 64 scores in registers, which frees
+//    the score buffer for the next tile's product while the exponentials run, and P
+//    has two buffers, so that neither product is waited for.  128-token tiles in one
+//    buffer need half the mma instructions for the scores (65 cycles each at N = 64 as
+//    at N = 128), but scores, softmax and product of a stream then follow one another:
+//    133 us against 73 us on 64 sequences of up to 4096 tokens with 32/8 heads.
 //  * The running maximum moves only when a score exceeds it by more than 2^8 in
 //    weight: O stays in TMEM and is rescaled a few times in a row's life instead of
 //    once a tile.  fp32 holds weights up to 2^8 as well as up to 1, and the
 //    quotient at the end does not depend on which reference was used.
 //  * STREAMS = 1 (up to 128 query rows, bound by HBM): two CTAs on an SM.  STREAMS = 2
 //    (more rows, bound by the products and the exponentials): two groups of 128 rows
-//    share each K and V tile, each with a thread of its own for the products.
-//  * Tiles of 64 tokens with two score buffers: the scores of the next tile are made
-//    while this one goes through the softmax.  One buffer of 128 tokens needs half
-//    the mma instructions (65 cycles each at N = 64 as at N = 128), but then scores,
-//    softmax and product of a stream follow one another: 6500 cycles for 128 tokens.
+//    share each K and V tile.
 //  * What a row does not see has no part in it.  Scores are replaced, not added
 //    to; V rows past the sequence's end are zeroed in shared memory before they meet
 //    a weight of zero; non-finite values of drafted V rows (which some rows see and
@@ -56,22 +58,24 @@ constexpr float kMaxRise = 8.0f;   // log2 of the largest weight before the refe
 template <int HEAD_DIM, int STREAMS>
 struct TreeCfg {
     static constexpr int kTileN = 64;                          // tokens of one tile
-    static constexpr uint32_t kBufs = 128 / kTileN;            // score buffers of a stream
+    static constexpr uint32_t kBufs = 2;                       // weight (P) buffers of a stream
     static constexpr int kBoxes = HEAD_DIM / 64;               // 128-byte wide column boxes
     static constexpr int kBoxBytes = kTileN * 128;             // one box of a K or V tile
     static constexpr int kTileBytes = kBoxes * kBoxBytes;
     static constexpr int kQBoxBytes = kTileM * 128;
     static constexpr int kQBytes = kBoxes * kQBoxBytes;        // one stream's queries
-    static constexpr uint32_t kSlots = STREAMS * (HEAD_DIM == 64 ? 8 : 4);  // ring depth
+    static constexpr uint32_t kSlots = STREAMS * (HEAD_DIM == 64 ? 4 : 2);  // tiles of K, and of V, in shared memory
     static constexpr uint32_t kMetas = 16;                     // tile descriptions
     static constexpr int kCtasPerSm = STREAMS == 1 ? 2 : 1;
     static constexpr int kSoftmaxWarps = 4 * STREAMS;
-    static constexpr int kThreads = (kSoftmaxWarps + 1 + STREAMS) * 32;  // + producer, product warps
-    // TMEM of one stream: the score buffers (P in the first half of each), then O.
+    static constexpr int kThreads = (kSoftmaxWarps + 2 + STREAMS) * 32;  // + producers of K and of V, product warps
+    // TMEM of one stream: the scores, two buffers of weights (bf16: half the columns), O.
+    static constexpr int kPCol = kTileN, kOCol = 128;
+    static_assert(kPCol + kBufs * kTileN / 2 <= kOCol, "TMEM columns of a stream");
     static constexpr int kStreamCols = 128 + 128;
     static constexpr int kCols = STREAMS * kStreamCols;
-    static constexpr uint32_t kBars = 2 * kSlots + 2 * kMetas + STREAMS * (2 * kBufs + 5);
-    static constexpr int kDataBytes = STREAMS * kQBytes + kSlots * kTileBytes;
+    static constexpr uint32_t kBars = 4 * kSlots + 2 * kMetas + STREAMS * (2 * kBufs + 6);
+    static constexpr int kDataBytes = STREAMS * kQBytes + 2 * kSlots * kTileBytes;
     // Each softmax warp turns its rows of the output into whole 64-byte pieces here.
     static constexpr int kStageBytes = kSoftmaxWarps * 2048;
     static constexpr int kTailBytes = kStageBytes + kMetas * 48 + kBars * 8 + 32 * 8 + 2 * 16 + 16 + 64 /* TreeSpot */;
@@ -428,16 +432,17 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
     TileMeta *meta = reinterpret_cast<TileMeta *>(stage + C::kStageBytes);
     TreeMark *mark = reinterpret_cast<TreeMark *>(meta + C::kMetas);  // [2]
     int64_t *scan = reinterpret_cast<int64_t *>(mark + 2);            // [32]
-    uint64_t *full = reinterpret_cast<uint64_t *>(scan + 32);
-    uint64_t *empty = full + kSlots;              // every stream has used the tile
-    uint64_t *meta_full = empty + kSlots;
+    uint64_t *full = reinterpret_cast<uint64_t *>(scan + 32);  // K's slots, then V's: the tile is there
+    uint64_t *empty = full + 2 * kSlots;          // every stream has used the tile
+    uint64_t *meta_full = empty + 2 * kSlots;
     uint64_t *meta_free = meta_full + C::kMetas;  // every softmax warp is done with the description
-    uint64_t *s_full = meta_free + C::kMetas;     // [stream][buffer]: scores are in TMEM
-    uint64_t *p_full = s_full + kBufs * STREAMS;  // [stream][buffer]: weights are in TMEM
-    uint64_t *q_full = p_full + kBufs * STREAMS;  // [stream]: the piece's queries are in shared memory
-    uint64_t *pv_done = q_full + STREAMS;         // [stream]: a tile has been added to O
-    uint64_t *o_done = pv_done + STREAMS;         // [stream]: a piece's last tile has
-    uint64_t *o_free = o_done + STREAMS;          // [stream]: a piece's O has been read
+    uint64_t *s_full = meta_free + C::kMetas;     // [stream]: scores are in TMEM
+    uint64_t *q_full = s_full + STREAMS;          // [stream]: the piece's queries are in shared memory
+    uint64_t *pv_done = q_full + STREAMS;         // [stream][buffer]: the buffer's tile has been added to O
+    uint64_t *o_done = pv_done + kBufs * STREAMS; // [stream]: a piece's last tile has
+    uint64_t *p_full = o_done + STREAMS;          // [stream][buffer]: weights are in TMEM
+    uint64_t *s_free = p_full + kBufs * STREAMS;  // [stream]: scores have been read
+    uint64_t *o_free = s_free + STREAMS;          // [stream]: a piece's O has been read
     uint64_t *drained = o_free + STREAMS;         // [stream]: every product has completed
     TreeSpot *spot = reinterpret_cast<TreeSpot *>(drained + STREAMS);
     static_assert(sizeof(TreeSpot) <= 64, "fits its place");
@@ -460,12 +465,11 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         uint64_t *bar = full + threadIdx.x;
         mbar_init(bar, bar >= empty && bar < meta_full       ? STREAMS
                        : bar >= meta_free && bar < s_full    ? C::kSoftmaxWarps
-                       : bar >= p_full && bar < q_full       ? 4
-                       : bar >= o_free && bar < drained      ? 4
+                       : bar >= p_full && bar < drained      ? 4
                                                              : 1);
         fence_mbar_init();
     }
-    if (warp == C::kSoftmaxWarps + 1) {
+    if (warp == C::kSoftmaxWarps + 2) {
         tmem_alloc(smem_addr(tmem_slot), C::kCols);
         tmem_relinquish();
         tc_fence_before();
@@ -475,13 +479,15 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
     if (p.part_o) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // The tiles of this CTA are numbered through all its pieces.  Items of the ring, in their order:
-    // K of the first kBufs tiles, then V(0) K(kBufs) V(1) K(kBufs + 1) ...
-    auto k_item = [](uint32_t t) { return t < kBufs ? t : 2 * t - kBufs + 1; };
-    auto v_item = [](uint32_t t) { return 2 * t + kBufs; };
-
-    if (warp == C::kSoftmaxWarps) {
-        // ---------------- producer: units, block-table dereference, TMA ----------------
+    // The tiles of this CTA are numbered through all its pieces: tile t has slot t of K's ring and of V's.
+    if (warp < C::kSoftmaxWarps + 2 && warp >= C::kSoftmaxWarps) {
+        // ---------------- producers: units, block-table dereference, TMA ----------------
+        // One warp for K, which also describes the tiles, one for V.  A copy costs the warp that issues it some
+        // 60 cycles, and a tile of 16-token pages is 16 copies: one warp for both took 2500 cycles a tile.
+        const bool is_k = warp == C::kSoftmaxWarps;
+        full += is_k ? 0 : kSlots;
+        empty += is_k ? 0 : kSlots;
+        ring += is_k ? 0 : kSlots * C::kTileBytes;
         const int pages = kTileN / p.block_size;  // of one tile
         const int page = lane / C::kBoxes, box = lane % C::kBoxes;
         const TreeMark end = mark[1];
@@ -556,15 +562,8 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             }
             return t;
         };
-        int landed = -1;  // lane s: the last item loaded into slot s
-        auto take_slot = [&](uint32_t it) {
-            const bool ok = it < kSlots || ring_wait<kSlots>(empty, it - kSlots, p.err_flag);
-            return (bool)__all_sync(0xffffffffu, ok);
-        };
-        auto load = [&](const Tile &t, bool is_k, uint32_t it) {
-            const uint32_t slot = it & (kSlots - 1);
+        auto load = [&](const Tile &t, uint32_t slot) {
             uint8_t *dst = ring + slot * C::kTileBytes;
-            if (lane == (int)slot) landed = (int)it;
             // V past the end is read from outside of the tensor, which gives zeros: whatever the ring held
             // must not meet a weight of zero.  (The rest of a partly used box is zeroed by the softmax warps.)
             if (t.flags & kTree) {
@@ -590,34 +589,31 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                             full + slot, policy);
             }
         };
-        // Tiles are drawn ahead of their loads, so that table entries are there when they are needed.
-        Tile t0{}, t1{}, older{};
-        uint32_t n = UINT32_MAX;  // tiles of this CTA, once known
+        // A tile is drawn one turn before it is loaded, so that table entries are there when they are needed.
+        int landed = -1;  // lane x: the last tile loaded into slot x
+        Tile next = next_tile();
 #pragma unroll 1
-        for (uint32_t t = UINT32_MAX;; ++t) {  // one turn before tile 0
-            older = t0;
-            t0 = t1;
-            t1 = next_tile();
-            if (t == UINT32_MAX) continue;
+        for (uint32_t t = 0;; ++t) {
+            Tile now = next;
+            if (!(now.flags & kEnd)) next = next_tile();
             // Everything that does not need the slot comes before the wait for it: in steady state the loads
             // wait for slots, and what lies between a free slot and its copy is lost.
-            const bool mine = n == UINT32_MAX;  // there is a description to publish
-            if (mine) {
-                const uint32_t holes = __ballot_sync(0xffffffffu, t0.mine && box == 0 && (t0.id < 0 || t0.id >= p.num_blocks));
+            if (is_k) {
+                const uint32_t holes = __ballot_sync(0xffffffffu, now.mine && box == 0 && (now.id < 0 || now.id >= p.num_blocks));
                 if (holes) {
                     if (lane == 0) raise_flag(p.err_flag, PA_FLAG_BAD_BLOCK);
-                    t0.flags &= ~kPlain;
+                    now.flags &= ~kPlain;
                 }
                 const uint32_t mt = t & (C::kMetas - 1);
                 const bool free = t < C::kMetas || ring_wait<C::kMetas>(meta_free, t - C::kMetas, p.err_flag);
                 if (!__all_sync(0xffffffffu, free)) break;
                 if (lane == 0) {
                     int4 *d = reinterpret_cast<int4 *>(meta + mt);
-                    d[0] = make_int4(t0.flags, t0.start, t0.valid, t0.dest);
-                    d[1] = make_int4(t0.first, t0.nodes, t0.node0, t0.h);
+                    d[0] = make_int4(now.flags, now.start, now.valid, now.dest);
+                    d[1] = make_int4(now.first, now.nodes, now.node0, now.h);
                 }
-                if (!(t0.flags & (kPlain | kEnd)) && lane < 4) {
-                    uint32_t bits = low_bits(t0.valid - 32 * lane);
+                if (!(now.flags & (kPlain | kEnd)) && lane < 4) {
+                    uint32_t bits = low_bits(now.valid - 32 * lane);
                     if (holes)
                         for (int x = 0; x < 32; ++x) {
                             const int at = (32 * lane + x) / p.block_size;
@@ -627,21 +623,15 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(meta_full + mt);
-                if (t0.flags & kEnd) {
-                    n = t;
-                } else {
-                    if (!take_slot(k_item(t))) break;
-                    load(t0, true, k_item(t));
-                }
             }
-            if (t >= kBufs - 1) {
-                const uint32_t u = t - (kBufs - 1);  // the tile whose V comes next
-                if (u >= n || !take_slot(v_item(u))) break;
-                load(kBufs == 1 ? t0 : older, false, v_item(u));
-            }
+            if (now.flags & kEnd) break;
+            const bool free = t < kSlots || ring_wait<kSlots>(empty, t - kSlots, p.err_flag);
+            if (!__all_sync(0xffffffffu, free)) break;
+            if (lane == (int)(t & (kSlots - 1))) landed = (int)t;
+            load(now, t & (kSlots - 1));
         }
         // If this CTA begins at the first cut inside a unit: how many pieces that unit has.
-        if (p.part_o && lane == 0) {
+        if (is_k && p.part_o && lane == 0) {
             TreeJoin j{0, 0, 0, 0, 0, {}};
             const TreeMark at = mark[0];
             if (at.b < p.batch && at.tile != 0) {
@@ -667,77 +657,67 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         }
         // Every copy has landed before the CTA ends (it has, unless a wait ran out).
         if (lane < (int)kSlots && landed >= 0) mbar_wait_bounded(full + lane, ((uint32_t)landed / kSlots) & 1, p.err_flag);
-    } else if (warp > C::kSoftmaxWarps) {
+    } else if (warp >= C::kSoftmaxWarps) {
         // ---------------- products, issued by one thread for each stream ----------------
-        // O += P V of tile t - kBufs, then S = Q K^T of tile t.
+        // S = Q K^T of tile t, then O += P V of tile t - 1.
         if (lane == 0) {
             constexpr uint32_t kQkDesc = tree_idesc(kTileN, false), kPvDesc = tree_idesc(HEAD_DIM, true);
-            const int s = warp - (C::kSoftmaxWarps + 1);
+            const int s = warp - (C::kSoftmaxWarps + 2);
             // Descriptors of the queries and of ring slot 0; a step through the operand or to another
             // slot adds to the start address (16-byte units), which never carries out of its field.
             const uint64_t q_desc = umma_desc_k_sw128(smem_addr(smem + s * C::kQBytes));
             const uint64_t k_desc = umma_desc_k_sw128(smem_addr(ring));
-            const uint64_t v_desc = umma_desc_mn_sw128(smem_addr(ring), C::kBoxBytes);
+            const uint64_t v_desc = umma_desc_mn_sw128(smem_addr(ring + kSlots * C::kTileBytes), C::kBoxBytes);
             const uint32_t base = tmem + s * C::kStreamCols;
             uint32_t scored = 0, added = 0;  // tiles whose scores / products were issued
             uint32_t pieces_q = 0, pieces_o = 0;
-            int queue[kBufs] = {};           // flags of the tiles between the two
-            auto wait_item = [&](uint32_t it) { return ring_wait<kSlots>(full, it, p.err_flag); };
-            bool ok = true, over = false;
-            for (uint32_t t = 0; ok; ++t) {
-                if (t >= kBufs) {
-                    const int f = queue[0];
-                    const uint32_t it = v_item(t - kBufs), slot = it & (kSlots - 1);
-                    if (f & kEnd) break;
-                    if (!(ok = wait_item(it))) break;
-                    if (s == 0 || (f & kTwo)) {
-                        const uint32_t g = added++;
-                        if (!(ok = ring_wait<kBufs>(p_full + kBufs * s, g, p.err_flag))) break;
-                        // a new piece overwrites O: the last one's has to have been read
-                        if ((f & kFirst) && pieces_o++ > 0 && !(ok = tree_wait(o_free + s, pieces_o & 1, p.err_flag))) break;
-                        tc_fence_after();
-                        const uint64_t vd = v_desc + slot * (C::kTileBytes / 16);
-                        const uint32_t a = base + (g & (kBufs - 1)) * kTileN;
-#pragma unroll
-                        for (int i = 0; i < kTileN / 16; ++i)
-                            umma_bf16_ts(base + 128, a + 8 * i, vd + i * (2048 / 16), kPvDesc, !(f & kFirst) || i > 0);
-                        umma_commit(pv_done + s);
-                        if (f & kLast) umma_commit(o_done + s);
-                        umma_commit(empty + slot);
-                    } else {
-                        mbar_arrive(empty + slot);
-                    }
-                }
-                int f = kEnd;
-                if (!over) {
-                    if (!(ok = ring_wait<C::kMetas>(meta_full, t, p.err_flag))) break;
-                    f = *const_cast<volatile int *>(&meta[t & (C::kMetas - 1)].flags);
-                    over = f & kEnd;
-                }
-                if (!over) {
-                    const uint32_t it = k_item(t), slot = it & (kSlots - 1);
-                    if (!(ok = wait_item(it))) break;
+            bool ok = true;
+            for (uint32_t t = 0, before = 0;; ++t) {
+                if (!(ok = ring_wait<C::kMetas>(meta_full, t, p.err_flag))) break;
+                const uint32_t f = *const_cast<volatile int *>(&meta[t & (C::kMetas - 1)].flags);
+                if (!(f & kEnd)) {
+                    const uint32_t slot = t & (kSlots - 1);
+                    if (!(ok = ring_wait<kSlots>(full, t, p.err_flag))) break;
                     if (s == 0 || (f & kTwo)) {
                         if ((f & kFirst) && !(ok = tree_wait(q_full + s, pieces_q++ & 1, p.err_flag))) break;
                         const uint32_t g = scored++;
-                        // the new scores take the place of an earlier tile's P: its product has to be done
-                        if (g >= kBufs && !(ok = tree_wait(pv_done + s, (g - kBufs) & 1, p.err_flag))) break;
+                        // the last scores have to be in registers
+                        if (g > 0 && !(ok = tree_wait(s_free + s, (g - 1) & 1, p.err_flag))) break;
                         tc_fence_after();
                         const uint64_t kd = k_desc + slot * (C::kTileBytes / 16);
-                        const uint32_t d = base + (g & (kBufs - 1)) * kTileN;
 #pragma unroll
                         for (int i = 0; i < HEAD_DIM / 16; ++i)
-                            umma_bf16_ss(d, q_desc + ((i >> 2) * C::kQBoxBytes + (i & 3) * 32) / 16,
+                            umma_bf16_ss(base, q_desc + ((i >> 2) * C::kQBoxBytes + (i & 3) * 32) / 16,
                                          kd + ((i >> 2) * C::kBoxBytes + (i & 3) * 32) / 16, kQkDesc, i > 0);
-                        umma_commit(s_full + kBufs * s + (g & (kBufs - 1)));
+                        umma_commit(s_full + s);
                         umma_commit(empty + slot);
                     } else {
                         mbar_arrive(empty + slot);
                     }
                 }
+                if (t > 0) {  // `before`: the last tile's flags
+                    const uint32_t slot = (t - 1) & (kSlots - 1);
+                    if (!(ok = ring_wait<kSlots>(full + kSlots, t - 1, p.err_flag))) break;
+                    if (s == 0 || (before & kTwo)) {
+                        const uint32_t g = added++, buf = g & (kBufs - 1);
+                        if (!(ok = ring_wait<kBufs>(p_full + kBufs * s, g, p.err_flag))) break;
+                        // a new piece overwrites O: the last one's has to have been read
+                        if ((before & kFirst) && pieces_o++ > 0 && !(ok = tree_wait(o_free + s, pieces_o & 1, p.err_flag))) break;
+                        tc_fence_after();
+                        const uint64_t vd = v_desc + slot * (C::kTileBytes / 16);
+                        const uint32_t a = base + C::kPCol + buf * (kTileN / 2);
 #pragma unroll
-                for (uint32_t x = 0; x + 1 < kBufs; ++x) queue[x] = queue[x + 1];
-                queue[kBufs - 1] = f;
+                        for (int i = 0; i < kTileN / 16; ++i)
+                            umma_bf16_ts(base + C::kOCol, a + 8 * i, vd + i * (2048 / 16), kPvDesc, !(before & kFirst) || i > 0);
+                        umma_commit(pv_done + kBufs * s + buf);
+                        if (before & kLast) umma_commit(o_done + s);
+                        umma_commit(empty + kSlots + slot);
+                    } else {
+                        mbar_arrive(empty + kSlots + slot);
+                    }
+                }
+                if (f & kEnd) break;
+                before = f;
             }
             umma_commit(drained + s);
             mbar_wait_bounded(drained + s, 0, p.err_flag);
@@ -747,7 +727,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         const int s = warp >> 2;
         const int r = threadIdx.x & (kTileM - 1);
         const uint32_t base = tmem + s * C::kStreamCols + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t o_addr = base + 128;
+        const uint32_t o_addr = base + C::kOCol;
         const float c = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;  // a scale of 0 must not meet -inf
         const float rise = kMaxRise / c;
 
@@ -800,8 +780,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                                    : w < p.words ? (uint32_t)__ldg(p.masks + (int64_t)(tile.first + node) * p.words + w)
                                                  : 0u;
             }
-            const uint32_t buf = g & (kBufs - 1);
-            ok = ring_wait<kBufs>(s_full + kBufs * s, g, p.err_flag);
+            ok = tree_wait(s_full + s, g & 1, p.err_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             if ((flags & kLast) && (warp & 3) == 0 && lane == 0) load_queries(t + 1);
             // the tokens of the tile that this row sees
@@ -828,11 +807,13 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             }
             __syncwarp();
             tc_fence_after();
-            const uint32_t s_addr = base + buf * kTileN;
             float x[kTileN];
 #pragma unroll
-            for (int q = 0; q < kTileN / 32; ++q) tmem_ld32(s_addr + 32 * q, x + 32 * q);
+            for (int q = 0; q < kTileN / 32; ++q) tmem_ld32(base + 32 * q, x + 32 * q);
             tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_free + s);  // the next tile's scores may be made
             if (!(flags & kPlain)) {
 #pragma unroll
                 for (int i = 0; i < kTileN; ++i) x[i] = (see[i >> 5] >> (i & 31)) & 1u ? x[i] : -INFINITY;
@@ -847,7 +828,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 m = next;
                 l *= down;
                 if (!(flags & kFirst)) {  // O has been written: wait for the last product, then rescale it
-                    ok = tree_wait(pv_done + s, (g - 1) & 1, p.err_flag);
+                    ok = ring_wait<kBufs>(pv_done + kBufs * s, g - 1, p.err_flag);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -861,6 +842,12 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                     }
                 }
             }
+            // the weights take the place of an earlier tile's: its product has to be done
+            const uint32_t buf = g & (kBufs - 1);
+            ok = g < kBufs || ring_wait<kBufs>(pv_done + kBufs * s, g - kBufs, p.err_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t p_addr = base + C::kPCol + buf * (kTileN / 2);
             const float bias = m == -INFINITY ? 0.f : -m * c;
             const float2 c2 = make_float2(c, c), bias2 = make_float2(bias, bias);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -874,21 +861,20 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                     sum[i & 1] = add2(sum[i & 1], pr);
                     w[i] = pack_bf16x2(pr.x, pr.y);
                 }
-                tmem_st16(s_addr + 16 * q, w);
+                tmem_st16(p_addr + 16 * q, w);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             if (!(flags & kPlain)) {
                 // What must not meet a weight of zero: the rows past the end of a partly used box become
                 // zeros, and values that are not finite leave drafted rows, which some rows do not see.
                 // Both streams share the work, and none of their rows goes on before it is done.  (The
-                // scores of tile t are there, so the slot's last V has been used up and the parity of
-                // `full` is that of V(t).)
+                // product of tile t - 2 is done, so what the slot held before V(t) has landed and the
+                // parity of `full` is that of V(t).)
                 const int valid = meta[mt].valid, box_rows = flags & kTree ? kTreeBox : p.block_size;
                 if ((flags & kTree) || (valid & (box_rows - 1))) {
-                    const uint32_t it = v_item(t);
-                    ok = ring_wait<kSlots>(full, it, p.err_flag);
+                    ok = ring_wait<kSlots>(full + kSlots, t, p.err_flag);
                     if (!__all_sync(0xffffffffu, ok)) break;
-                    const uint32_t v0 = smem_addr(ring) + (it & (kSlots - 1)) * C::kTileBytes;
+                    const uint32_t v0 = smem_addr(ring) + (kSlots + (t & (kSlots - 1))) * C::kTileBytes;
                     const int end = (valid + box_rows - 1) & -box_rows;
                     const bool two = STREAMS == 2 && (flags & kTwo);
                     const int at = two ? threadIdx.x : r, rows = two ? 32 : 16;  // a row is eight chunks
@@ -1028,7 +1014,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == C::kSoftmaxWarps + 1) {
+    if (warp == C::kSoftmaxWarps + 2) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kCols);
     }
