@@ -596,6 +596,7 @@ int pa_tree_masks(int32_t *masks, int32_t *positions, const int32_t *parents, co
  * scale          : finite and not negative (else PA_ERR_INVALID_ARG)
  * workspace      : pa_decode_tree_workspace_size(...) bytes, 16-byte aligned
  *                  (may be NULL if that is 0); no initialisation needed.
+ *                  Calls that may overlap on the GPU need one each.
  * A block id outside [0, num_blocks) sets PA_FLAG_BAD_BLOCK and its tokens
  * are left out.  Other arguments, layouts and errors: as pa_decode.
  * Products take bf16 operands and accumulate in fp32; the softmax is fp32. */

@@ -17,7 +17,9 @@ namespace {
 // kPlanThreads sequences at a time.
 constexpr int kPlanThreads = 1024;
 // Rows that the planning CTA maps itself; more rows go to a second launch over
-// the whole GPU.
+// the whole GPU.  Measured (64 sequences, calls back to back): 512 rows 6.2 us of
+// GPU time here, 8.3 with the second launch; 4096 rows 8.3 and 8.2, of which the
+// host's 9.7 and 11.8 hide both; 8192 rows 12.4 and 8.3; 32768 rows 36 and 8.3.
 constexpr int kPlanRows = 4 * kPlanThreads;
 constexpr int kMapThreads = 256;
 
@@ -120,13 +122,15 @@ __device__ __forceinline__ void map_row(const ExtendParams &p, int r) {
     if (p.positions) p.positions[r] = at;
 }
 
+// 14 us together with the mapping launch for 64 prompts of up to 4096 tokens (131072 rows, 0.2 us of bytes): each
+// step of the plan waits for the one before (lengths, sums, list, table, sums, slots).
 // Pass 1 adds up the tokens and blocks of all sequences; pass 2 scans them again
 // and writes lengths, counts and table entries.  Batches of up to kPlanThreads
 // sequences stay in registers between the two.
 __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan_kernel(const ExtendParams p) {
     __shared__ int s_blk[kPlanThreads + 1];  // blocks taken before each sequence of this chunk
     __shared__ int s_old[kPlanThreads];      // entries its table had
-    const int cursor = __ldg(p.cursor);
+    const int cursor = *p.cursor;  // may be cursor_out
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
     int len = 0, add = 0, blocks = 0;
     int64_t tok_before = 0, blk_before = 0, tok_total, blk_total;
@@ -200,6 +204,7 @@ __global__ void __launch_bounds__(kMapThreads) extend_map_kernel(const ExtendPar
 
 constexpr int kMaskThreads = 256;
 
+// 6.2 us for 256 trees of up to 256 nodes (0.3 us of bytes; an empty launch of this size takes 4).
 // One CTA for each sequence: every thread walks the ancestors of its nodes, which
 // takes as many steps as the tree is deep, and sets their bits in a mask row of
 // its own.  CTA `batch` clears the rows that belong to no sequence.
@@ -265,7 +270,8 @@ int pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq, const int32_
         return PA_ERR_INVALID_ARG;
     if (!pa::supported_block_size(block_size)) return PA_ERR_UNSUPPORTED;
     if (num_blocks > INT32_MAX / block_size) return PA_ERR_INVALID_ARG;  // a slot is an int32
-    if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX) return PA_ERR_INVALID_ARG;  // a length is an int32
+    // a length is an int32, and so is one rounded up to whole blocks
+    if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - block_size) return PA_ERR_INVALID_ARG;
     if ((cu_rows == nullptr) != (path == nullptr)) return PA_ERR_INVALID_ARG;
     if (batch == 0) return PA_OK;
     if (!seq_lens || !add_lens || !seq_lens_out || !free_cursor || !free_cursor_out || !cu_tokens)

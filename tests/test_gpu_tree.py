@@ -357,6 +357,81 @@ def test_streams_graphs_and_a_shared_workspace():
     cases[0].check(outs[0])
 
 
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 16, 2), (64, 8, 1), (128, 4, 1)])
+@pytest.mark.parametrize("pt", [-1, 128, 0])
+def test_trees_of_one_and_of_two_row_groups_in_turn(d, Hq, Hkv, pt):
+    """Trees whose rows fill one group of 128, two of them or several pairs follow each other on one SM."""
+    c = Case([300, 1200, 77, 900, 640, 64, 2000, 0, 513], [33, 3, 40, 0, 17, 64, 1, 16, 48], Hq, Hkv, d, 16, seed=d + Hq,
+             tail=1)
+    c.check(c.launch(pt, fill=255))
+    assert c.flag == 0
+
+
+def test_two_row_groups_for_trees_of_one():
+    """max_nodes calls for two groups of rows, no tree has more than one; a width of masks beyond every tree."""
+    c = Case([700, 130, 1, 64], [5, 16, 1, 9], 8, 1, 128, 16, seed=12, extra_words=3)
+    c.check(c.launch(128))
+    assert c.flag == 0
+
+
+def test_more_sequences_than_threads():
+    rng = np.random.default_rng(5)
+    c = Case(rng.integers(0, 90, 1203), rng.integers(0, 3, 1203), 4, 2, 64, 8, seed=5)
+    c.check(c.launch(-1))
+    c.check(c.launch(128, max_len=600))  # room for cuts, of which each unit is too short
+    assert c.flag == 0
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace of its own, while both are at work."""
+    import torch
+    import paged_kv_cache_349_b200 as pa
+    cases = [Case([3000, 900], [16, 9], 8, 2, 128, 16, seed=1), Case([2500, 1800], [64, 30], 8, 1, 128, 16, seed=2)]
+    want = [c.launch(128) for c in cases]
+    jobs = []
+    for c in cases:
+        dev = [x.contiguous().cuda() for x in (c.q, c.kt, c.vt, c.k, c.v)] + [i32_dev(x) for x in
+                                                                             (c.tables, c.lens, c.cu, c.masks)]
+        size = pa.pa_decode_tree_workspace_size(2, c.T, c.Hq, c.Hkv, 128, 16, c.max_len, c.max_nodes, 128)
+        jobs.append((c, dev, torch.empty(size, dtype=torch.uint8, device="cuda"),
+                     [torch.empty(c.T, c.Hq, 128, dtype=torch.bfloat16, device="cuda") for _ in range(20)],
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, dev, ws, outs, stream in jobs:
+            pa.pa_decode_tree(outs[i], *dev, max_seq_len=c.max_len, max_nodes=c.max_nodes, scale=c.scale,
+                              partition_tokens=128, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for (c, dev, ws, outs, stream), w in zip(jobs, want):
+        assert all(torch.equal(o, w) for o in outs)
+
+
+def test_pool_offsets_past_32_bits():
+    """Blocks at the end of pools of more than 2^31 values, read here and written by pa_rope_and_cache."""
+    import torch
+    import paged_kv_cache_349_b200 as pa
+    c = Case([300, 45], [9, 4], 16, 8, 128, 16, seed=3)
+    small = c.launch(128)
+    total = 2 ** 31 // (8 * 16 * 128) + 64
+    pools = [torch.empty(total, 8, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for pool, part in zip(pools, (c.k, c.v)):
+        pool[total - c.nb:] = part.cuda()
+    tables = i32_dev(c.tables + (total - c.nb))
+    size = pa.pa_decode_tree_workspace_size(2, c.T, 16, 8, 128, 16, c.max_len, c.max_nodes, 128)
+    ws = torch.empty(max(size, 16), dtype=torch.uint8, device="cuda")
+    out = torch.empty(c.T, 16, 128, dtype=torch.bfloat16, device="cuda")
+    pa.pa_decode_tree(out, c.q.contiguous().cuda(), c.kt.contiguous().cuda(), c.vt.contiguous().cuda(), *pools, tables,
+                      i32_dev(c.lens), i32_dev(c.cu), i32_dev(c.masks), max_seq_len=c.max_len, max_nodes=c.max_nodes,
+                      scale=c.scale, partition_tokens=128, workspace=ws)
+    assert torch.equal(out, small)
+    k, v = c.kt.contiguous().cuda(), c.vt.contiguous().cuda()
+    slots = torch.arange(total * 16 - c.T, total * 16, dtype=torch.int32, device="cuda")
+    turns, _ = pa.pa_rope_frequencies(128)
+    pa.pa_rope_and_cache(None, None, k, v, *pools, slots, torch.zeros_like(slots), turns.cuda())  # position 0: no turn
+    for pool, rows in zip(pools, (k, v)):
+        assert torch.equal(pool[-2:].transpose(1, 2).reshape(32, 8, 128)[32 - c.T:], rows)
+
+
 def test_python_refusals():
     import torch
     import paged_kv_cache_349_b200 as pa

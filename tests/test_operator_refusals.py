@@ -66,7 +66,7 @@ def test_extend_tables_refusals():
                   path=None, maxp=0, flag=None, stream=None)
     assert call(B=0) == OK
     for bad in (dict(B=-1), dict(T=-1), dict(maxb=-1), dict(NB=0), dict(nfree=-1), dict(maxp=-1), dict(cu_rows=ptr()),
-                dict(path=ptr()), dict(NB=1 << 28), dict(maxb=1 << 28)):
+                dict(path=ptr()), dict(NB=1 << 28), dict(maxb=1 << 28), dict(maxb=(1 << 27) - 1)):
         assert call(**bad) == INVALID, bad
     for name in ("bt", "lens", "add", "lens_out", "free", "cur", "cur_out", "slots", "cu"):
         assert call(**{name: None}) == INVALID, name
