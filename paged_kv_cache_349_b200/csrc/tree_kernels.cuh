@@ -240,9 +240,10 @@ __device__ __forceinline__ bool ring_wait(uint64_t *bars, uint32_t n, int32_t *f
     return tree_wait(bars + (n & (N - 1)), (n / N) & 1, flag);
 }
 
-// Whether either bf16 of w is an infinity or NaN.
-__device__ __forceinline__ bool not_finite2(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Whether any bf16 of v is an infinity or NaN (0: none is): an exponent of ones carries into the sign's place.
+__device__ __forceinline__ uint32_t not_finite8(const uint4 &v) {
+    auto test = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
+    return (test(v.x) | test(v.y) | test(v.z) | test(v.w)) & 0x80008000u;
 }
 // w with the halves that are not finite set to zero.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
@@ -882,25 +883,37 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                     const int end = (valid + box_rows - 1) & -box_rows;
                     const bool two = STREAMS == 2 && (flags & kTwo);
                     const int at = two ? threadIdx.x : r, rows = two ? 32 : 16;  // a row is eight chunks
-                    bool odd = false;
+                    const uint32_t mine = v0 + (at >> 3) * 128 + (at & 7) * 16;
+                    auto put = [](uint32_t addr, const uint4 &v) {
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+                                     "r"(v.w)
+                                     : "memory");
+                    };
 #pragma unroll 1
-                    for (int row = (flags & kTree ? 0 : valid) + (at >> 3); row < end; row += rows) {
+                    for (int row = valid + (at >> 3); row < end; row += rows)
 #pragma unroll
-                        for (int x = 0; x < C::kBoxes; ++x) {
-                            const uint32_t addr = v0 + x * C::kBoxBytes + row * 128 + (at & 7) * 16;
-                            uint4 v = lds128(addr);
-                            const bool bad = not_finite2(v.x) || not_finite2(v.y) || not_finite2(v.z) || not_finite2(v.w);
-                            if (row >= valid)
-                                v = make_uint4(0u, 0u, 0u, 0u);
-                            else if (bad)
-                                v = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
-                            else
-                                continue;
-                            odd |= row < valid;
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
-                                         "r"(v.z), "r"(v.w)
-                                         : "memory");
-                        }
+                        for (int x = 0; x < C::kBoxes; ++x)
+                            put(mine + (row - (at >> 3)) * 128 + x * C::kBoxBytes, make_uint4(0u, 0u, 0u, 0u));
+                    bool odd = false;
+                    if (flags & kTree) {
+                        // All loads at once, one test for all of them; looked at one by one only if it says so.
+                        uint32_t bad = 0;
+#pragma unroll
+                        for (int k = 0; k < kTileN; k += 16)
+                            if (k / 16 * rows + (at >> 3) < valid)
+#pragma unroll
+                                for (int x = 0; x < C::kBoxes; ++x)
+                                    bad |= not_finite8(lds128(mine + k / 16 * rows * 128 + x * C::kBoxBytes));
+                        odd = bad != 0;
+                        if (odd)
+#pragma unroll 1
+                            for (int row = at >> 3; row < valid; row += rows)
+#pragma unroll 1
+                                for (int x = 0; x < C::kBoxes; ++x) {
+                                    const uint32_t addr = mine + (row - (at >> 3)) * 128 + x * C::kBoxBytes;
+                                    const uint4 v = lds128(addr);
+                                    put(addr, make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w)));
+                                }
                     }
                     // A barrier of its own for one and for two streams: the second stream skips tiles without
                     // rows of its own.  Two cleanings of a kind take turns with the word that says what was found.
