@@ -93,9 +93,10 @@ struct TreeMark {
     int b, unit, tile;
 };
 
-// What the second kernel joins: the pieces of the unit whose first cut is where a CTA begins (0: none).
+// What the second kernel joins: the unit inside which a CTA begins (0 pieces: it begins with a unit), and the first of
+// the CTAs that begin inside it.
 struct __align__(16) TreeJoin {
-    int pieces, first, nodes, node0, h, pad[3];
+    int pieces, cut0, first, nodes, node0, h, pad[2];
 };
 
 struct TreeParams {
@@ -619,30 +620,38 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             if (lane == (int)(t & (kSlots - 1))) landed = (int)t;
             load(now, t & (kSlots - 1));
         }
-        // If this CTA begins at the first cut inside a unit: how many pieces that unit has.
-        if (is_k && p.part_o && lane == 0) {
-            TreeJoin j{0, 0, 0, 0, 0, {}};
+        // If this CTA begins inside a unit: which others do, that is, how many pieces the unit has.
+        if (is_k && p.part_o) {
+            TreeJoin j{0, 0, 0, 0, 0, 0, {}};
             const TreeMark at = mark[0];
             if (at.b < p.batch && at.tile != 0) {
                 const TreeSeq q = tree_seq(p, at.b);
                 const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, q);
+                const TreeLine &line = spot->line;
                 auto inside = [&](int i) {  // cut i is one of this unit
-                    if (i >= spot->line.count) return false;
-                    const int64_t x = tree_cut(spot->line, i) - spot->begin;
+                    if (i < 0 || i >= line.count) return false;
+                    const int64_t x = tree_cut(line, i) - spot->begin;
                     if (x < 0 || x >= u.tiles + C::kUnitCost) return false;
                     const TreeMark m = tree_mark<HEAD_DIM, STREAMS>(p, u, at.b, x);
                     return m.unit == 0 && m.tile != 0;
                 };
-                if (!inside((int)blockIdx.x - 1)) {
-                    j.pieces = 2;
-                    while (inside((int)blockIdx.x + j.pieces - 1)) ++j.pieces;
-                    j.first = q.first;
-                    j.nodes = q.nodes;
-                    j.h = at.unit / u.chunks;
-                    j.node0 = (at.unit - j.h * u.chunks) * (STREAMS * tile_nodes);
-                }
+                auto run = [&](int from, int by) {  // cuts from, from + by, ... that are
+                    int n = 0;
+                    for (;;) {
+                        const uint32_t is = __ballot_sync(0xffffffffu, inside(from + by * (n + lane)));
+                        if (is != 0xffffffffu) return n + __ffs(~is) - 1;
+                        n += 32;
+                    }
+                };
+                const int before = run((int)blockIdx.x - 1, -1);
+                j.pieces = before + run((int)blockIdx.x + 1, 1) + 2;
+                j.cut0 = (int)blockIdx.x - before;
+                j.first = q.first;
+                j.nodes = q.nodes;
+                j.h = at.unit / u.chunks;
+                j.node0 = (at.unit - j.h * u.chunks) * (STREAMS * tile_nodes);
             }
-            p.joins[blockIdx.x] = j;
+            if (lane == 0) p.joins[blockIdx.x] = j;
         }
         // Every copy has landed before the CTA ends (it has, unless a wait ran out).
         if (lane < (int)kSlots && landed >= 0) mbar_wait_bounded(full + lane, ((uint32_t)landed / kSlots) & 1, p.err_flag);
@@ -1047,23 +1056,42 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
 
 // Joins the states of the units that were cut:
 //   out = sum_p 2^(m_p - M) l_p o_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p.
-// CTA (i, y): if cut i + 1 is the first one inside its unit, rows [32 y, 32 y + 32) of that unit.  The
-// piece before the first cut is CTA i's second state, the pieces after the cuts are the first states of
-// the CTAs that begin there.  Four rows of a warp are in flight at once.
+// CTA (i, y) belongs to the unit inside which cut i + 1 lies.  Where a unit has few pieces the CTAs of its first cut
+// join it, 32 rows each, four to a warp.  More pieces have the CTAs of all its cuts, and where that leaves warps over,
+// several take the same rows and a part of the pieces each: a sequence alone on the GPU is cut into 40 pieces, and a
+// warp that goes through all of them waits for 20 loads in a row (4 sequences of up to 10364 tokens with 8/2 heads of
+// 64: 53 us for the whole call, now 31).  The piece before the first cut is the second state of the CTA before, the
+// pieces after the cuts are the first states of the CTAs that begin there.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinRows = 32;
+// Pieces that a warp joins alone: where all CTAs of the grid are on the GPU at once, and where they are not and the
+// CTAs of the other cuts would only be in the way.  Measured with 4 | 8 for both: 8 sequences of 32768 tokens with 128
+// rows of each kv head (two waves) 196 | 193 us; 2 of up to 13545 with 40/40 heads and 16 rows 62 | 65 us.
+constexpr int kJoinAlone = 3, kJoinAloneWaves = 8;
 
 template <int HEAD_DIM, int STREAMS>
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) tree_join_kernel(const TreeParams p) {
     constexpr int V = HEAD_DIM / 32, R = kJoinRows / kJoinWarps;
     constexpr int kRows = STREAMS * kTileM;
+    __shared__ float s_acc[kJoinWarps][R][HEAD_DIM];
+    __shared__ float s_state[kJoinWarps][R][3];  // M, den, none
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = blockIdx.x + 1;
+    const int cut = blockIdx.x + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const TreeJoin j = p.joins[first];
-    const int node0 = j.node0, pieces = j.pieces, h = j.h;
-    const int r0 = blockIdx.y * kJoinRows + warp * R;
-    if (pieces == 0 || node0 + (r0 >> p.group_shift) >= j.nodes) return;
+    const TreeJoin *unit = p.joins + cut;
+    const int pieces = unit->pieces, first = unit->cut0;
+    constexpr unsigned kWave = STREAMS == 1 ? 2 : 4;  // rows of this grid that fit the GPU
+    const bool shared = pieces > (gridDim.y <= kWave ? kJoinAlone : kJoinAloneWaves);
+    if (pieces == 0 || (!shared && cut != first)) return;  // the whole CTA
+    const int rows = min((unit->nodes - unit->node0) << p.group_shift, kRows);
+    int each = 1;  // warps that share a group of R rows
+    int r0 = ((int)blockIdx.y * kJoinWarps + warp) * R;
+    if (shared) {
+        const int ctas = (pieces - 1) * (int)gridDim.y, groups = (rows + R - 1) / R;
+        while (each < kJoinWarps && groups * 2 * each <= ctas * kJoinWarps) each *= 2;
+        r0 = (((cut - first) * (int)gridDim.y + (int)blockIdx.y) * kJoinWarps + warp) / each * R;
+    }
+    if (r0 >= rows && each == 1) return;
     // state of piece k: 2 * first - 1, then 2 * first, 2 * first + 2, ...
     auto state = [&](int k) { return (int64_t)(k == 0 ? 2 * first - 1 : 2 * (first + k - 1)) * kRows + r0; };
     float M[R], den[R], none[R], acc[R][V];
@@ -1075,7 +1103,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) tree_join_kernel(const Tre
         for (int e = 0; e < V; ++e) acc[r][e] = 0.f;
     }
 #pragma unroll 2
-    for (int k = 0; k < pieces; ++k) {
+    for (int k = r0 < rows ? warp & (each - 1) : pieces; k < pieces; k += each) {
         float2 ml[R];
         float o[R][V];
         // rows past the last node hold whatever the workspace held: they are not stored below
@@ -1105,12 +1133,36 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) tree_join_kernel(const Tre
             for (int e = 0; e < V; ++e) acc[r][e] = acc[r][e] * down + w * o[r][e];
         }
     }
+    if (each > 1) {  // the sums so far are states of their own
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) s_acc[warp][r][lane * V + e] = acc[r][e];
+            if (lane < 3) s_state[warp][r][lane] = lane == 0 ? M[r] : lane == 1 ? den[r] : none[r];
+        }
+        __syncthreads();
+        if ((warp & (each - 1)) != 0 || r0 >= rows) return;
+#pragma unroll 1
+        for (int w = warp + 1; w < warp + each; ++w)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float m = s_state[w][r][0], top = fmaxf(M[r], m);
+                none[r] += s_state[w][r][2];
+                if (m == -INFINITY) continue;
+                const float down = fast_exp2(M[r] - top), up = fast_exp2(m - top);
+                M[r] = top;
+                den[r] = den[r] * down + up * s_state[w][r][1];
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[r][e] = acc[r][e] * down + up * s_acc[w][r][lane * V + e];
+            }
+    }
+    const int node0 = unit->node0, head0 = unit->h * p.group, row0 = unit->first, nodes = unit->nodes;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int row = r0 + r, node = node0 + (row >> p.group_shift);
-        if (node >= j.nodes) break;
+        if (node >= nodes) break;
         uint32_t *dst = reinterpret_cast<uint32_t *>(
-            p.out + ((int64_t)(j.first + node) * p.q_heads + h * p.group + (row & (p.group - 1))) * HEAD_DIM + lane * V);
+            p.out + ((int64_t)(row0 + node) * p.q_heads + head0 + (row & (p.group - 1))) * HEAD_DIM + lane * V);
 #pragma unroll
         for (int e = 0; e < V; e += 2)
             dst[e / 2] = M[r] == -INFINITY ? pack_bf16x2(none[r], none[r]) : pack_bf16x2(acc[r][e] / den[r], acc[r][e + 1] / den[r]);

@@ -256,6 +256,17 @@ def test_split_over_a_long_cache(pt):
         c.check(c.launch(pt, fill=fill))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,counts,Hq", [([9000], [3], 2), ([9000], [20], 8), ([5001, 3, 3000], [5, 1, 33], 8), ([4000], [0], 4),
+                                            ([9000], [9], 8)])
+def test_many_pieces_of_one_unit(d, lens, counts, Hq):
+    """Few rows and a long cache: dozens of pieces to join, more than there are rows."""
+    c = Case(lens, counts, Hq, 1, d, 16, seed=d + Hq, tail=2)
+    for fill in (0, 255):
+        c.check(c.launch(128, fill=fill))
+        assert c.flag == 0
+
+
 def test_results_do_not_depend_on_placement_or_neighbours():
     """Bit-identical when blocks move and when a sequence runs alone."""
     import torch
