@@ -82,8 +82,10 @@ struct TreeCfg {
     static constexpr int kSmemBytes = 1024 /* align slack */ + kDataBytes + kTailBytes;
     static_assert(kCtasPerSm * kCols <= 512, "TMEM columns of an SM");
     static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
-    // What a unit costs besides its tiles (its output, and tiles that are not whole: 4 us measured, a tile
-    // 1.3 us), and the shortest pieces worth cutting off, in tiles.
+    // What a unit costs besides its tiles (its output, and tiles that are not whole: 3 to 4 us, a tile 1.1 us), and
+    // the shortest pieces worth cutting off, in tiles.  Measured on 64 sequences of up to 4096 tokens with 32/8 heads
+    // | 24 of up to 2048 with 32/32, in us: 2 and 2 72.7 | 77.5, 3 and 2 70.2 | 78.4, 4 and 2 70.8 | 79.7, 3 and 1
+    // 70.5 | 78.4, 3 and 3 70.2 | 79.7.
     static constexpr int kUnitCost = 3;
     static constexpr int kSnap = 2;
 };
