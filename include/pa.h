@@ -535,7 +535,9 @@ int pa_decode_append_fp8(float *out, const void *q, const void *k_new, const voi
  *            < -1) sets PA_FLAG_BAD_TREE and reads as -1.
  * cu_nodes : device int32 [batch + 1], cu_nodes[0] <= ... <= cu_nodes[batch];
  *            bounds that decrease or leave [0, num_rows] are cut and set
- *            PA_FLAG_BAD_LEN.
+ *            PA_FLAG_BAD_LEN.  A row has one owner: sequence b's begin at the
+ *            largest of the bounds up to its own, and a sequence whose own is
+ *            below that has no nodes.
  * seq_lens : device int32 [batch], the tokens already cached
  * max_nodes: at least every sequence's node count, at most
  *            PA_TREE_MAX_NODES (else PA_ERR_UNSUPPORTED).  Nodes from

@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(
     extern __shared__ int32_t s_tree[];
     int32_t *s_parent = s_tree;             // [max_nodes]
     int32_t *s_mask = s_tree + max_nodes;   // [max_nodes, words]
+    __shared__ int s_floor;
     const int b = blockIdx.x;
     auto bound = [&](int i) { return min(max(__ldg(cu + i), 0), num_rows); };
     auto clear = [&](int lo, int hi) {
@@ -222,14 +223,26 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(
         if (positions)
             for (int r = lo + threadIdx.x; r < hi; r += kMaskThreads) positions[r] = 0;
     };
+    // Each row is written by one CTA, whatever the bounds: the rows of CTA b begin at the largest of bounds 0 .. b.
+    // A sequence that begins below an earlier bound would lose its first nodes there and is left without any.
+    const int lo = bound(b);
+    int top = 0;
+    for (int j = threadIdx.x; j < b; j += kMaskThreads) top = max(top, bound(j));
+    if (threadIdx.x == 0) s_floor = 0;
+    int start = lo;
+    if (__syncthreads_or(top > lo)) {
+        atomicMax(&s_floor, top);
+        __syncthreads();
+        start = s_floor;
+    }
     if (b == batch) {
         clear(0, bound(0));
-        clear(max(bound(0), bound(batch)), num_rows);
+        clear(start, num_rows);
         return;
     }
-    const int lo = bound(b), hi = max(bound(b + 1), lo);
-    const int n = min(hi - lo, max_nodes);
-    if (threadIdx.x == 0 && (lo != __ldg(cu + b) || hi != __ldg(cu + b + 1) || n != hi - lo))
+    const int end = max(bound(b + 1), start);
+    const int n = start == lo ? min(end - start, max_nodes) : 0;
+    if (threadIdx.x == 0 && (start != __ldg(cu + b) || end != __ldg(cu + b + 1) || n != end - start))
         raise_flag(err_flag, PA_FLAG_BAD_LEN);
     for (int i = threadIdx.x; i < n; i += kMaskThreads) {
         int parent = __ldg(parents + lo + i);
@@ -252,7 +265,7 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(
     }
     __syncthreads();
     for (int x = threadIdx.x; x < n * words; x += kMaskThreads) masks[(int64_t)lo * words + x] = s_mask[x];
-    clear(lo + n, hi);
+    clear(start + n, end);
 }
 
 }  // namespace

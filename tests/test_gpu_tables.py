@@ -254,3 +254,38 @@ def test_tree_masks_bad_input(cu, parents, max_nodes, flag):
         assert host(masks)[:, 0].tolist() == [1, 3, 7, 0, 0, 1] and host(pos).tolist() == [10, 11, 12, 0, 0, 20]
     elif cu[0] == -2:
         assert host(masks)[:, 0].tolist() == [1, 3, 7, 1, 3, 7] and host(pos).tolist() == [10, 11, 12, 20, 21, 22]
+
+
+@pytest.mark.parametrize("cu,bits,positions", [
+    ([4, 2, 6], [0, 0, 0, 0, 0, 0], [0, 0, 0, 0, 0, 0]),
+    ([0, 5, 3, 8], [1, 3, 7, 15, 31, 0, 0, 0], [10, 11, 12, 13, 14, 0, 0, 0]),
+    ([2, 4, 1, 3, 4, 7], [0, 0, 1, 3, 1, 3, 7], [0, 0, 10, 11, 50, 51, 52]),
+    ([6, 6, 0, 6], [0] * 6, [0] * 6),
+])
+def test_tree_masks_bounds_that_decrease(cu, bits, positions):
+    """Every row has one owner: a sequence that begins below an earlier bound has no nodes."""
+    import torch
+    import paged_kv_cache_349_b200 as pa
+    T, B = len(bits), len(cu) - 1
+    parents = [x.bit_length() - 2 if x else -1 for x in bits]  # chains
+    for _ in range(20):
+        masks, pos, flag = torch.full((T, 1), -1, dtype=torch.int32, device="cuda"), i32_dev(np.full(T, 9)), i32_dev([0])
+        pa.pa_tree_masks(masks, pos, i32_dev(parents), i32_dev(cu), i32_dev(10 * np.arange(1, B + 1)), max_nodes=8,
+                         err_flag=flag)
+        assert int(flag.item()) == pa.PA_FLAG_BAD_LEN
+        assert host(masks)[:, 0].tolist() == bits and host(pos).tolist() == positions
+
+
+def test_tree_masks_of_more_sequences_than_threads():
+    """One early bound that is too large takes the rows of all sequences below it, of none above."""
+    import torch
+    import paged_kv_cache_349_b200 as pa
+    B = 700
+    cu = np.arange(B + 1)
+    cu[3] = 600
+    masks, pos, flag = torch.full((B, 1), -1, dtype=torch.int32, device="cuda"), i32_dev(np.full(B, 9)), i32_dev([0])
+    pa.pa_tree_masks(masks, pos, i32_dev(np.full(B, -1)), i32_dev(cu), i32_dev(np.arange(B)), max_nodes=1, err_flag=flag)
+    want, wpos = np.ones(B, int), np.arange(B)
+    want[3:600] = wpos[3:600] = 0  # row 2 is the first node of the sequence that ends at 600
+    assert int(flag.item()) == pa.PA_FLAG_BAD_LEN
+    assert np.array_equal(host(masks)[:, 0], want) and np.array_equal(host(pos), wpos)
