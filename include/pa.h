@@ -581,7 +581,8 @@ int pa_tree_masks(int32_t *masks, int32_t *positions, const int32_t *parents, co
  * seq_lens       : device int32 [batch], cached tokens, the drafted ones not
  *                  counted
  * cu_nodes       : as in pa_tree_masks.  Rows past max_nodes of a sequence
- *                  set PA_FLAG_BAD_LEN and are left as they were.
+ *                  set PA_FLAG_BAD_LEN and are left as they were, as are rows
+ *                  that belong to no sequence because bounds decrease.
  * masks          : device int32 [num_rows, ceil(max_nodes / 32)], any bits
  *                  (pa_tree_masks gives those of a tree); bits past the
  *                  sequence's nodes are not looked at.  NULL: a chain, node i

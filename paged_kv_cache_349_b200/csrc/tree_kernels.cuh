@@ -90,9 +90,10 @@ struct TreeCfg {
     static constexpr int kSnap = 2;
 };
 
-// Where a CTA's share begins: tile `tile` of unit `unit` of sequence `b` (b = batch: nowhere).
+// Where a CTA's share begins: tile `tile` of unit `unit` of sequence `b` (b = batch: nowhere), whose rows begin at
+// `floor` or later.
 struct TreeMark {
-    int b, unit, tile;
+    int b, unit, tile, floor;
 };
 
 // What the second kernel joins: the unit inside which a CTA begins (0 pieces: it begins with a unit), and the first of
@@ -255,19 +256,25 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
     return w;
 }
 
-// The sequence of a CTA, as every kernel of one call sees it.
+// A bound between sequences' rows.
+__device__ __forceinline__ int tree_bound(const TreeParams &p, int i) { return min(max(__ldg(p.cu + i), 0), p.num_rows); }
+
+// The sequence of a CTA, as every kernel of one call sees it.  Each row has one owner, whatever the bounds: `floor` is
+// the largest of the bounds before b (where no bound is below the one before it, 0 does as well), and a sequence that
+// begins below it has no nodes.
 struct TreeSeq {
     int first, nodes, len;
+    int end;  // the floor of the next sequence
     bool bad;
 };
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b) {
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b, int floor) {
     const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1), raw = __ldg(p.lens + b);
     TreeSeq s;
     s.first = min(max(lo, 0), p.num_rows);
-    const int end = max(min(max(hi, 0), p.num_rows), s.first);
-    s.nodes = min(end - s.first, p.max_nodes);
+    s.end = max(min(max(hi, 0), p.num_rows), max(s.first, floor));
+    s.nodes = s.first < floor ? 0 : min(s.end - s.first, p.max_nodes);
     s.len = min(max(raw, 0), min(p.max_seq_len, p.max_blocks * p.block_size));
-    s.bad = s.first != lo || end != hi || s.nodes != end - s.first || s.len != raw;
+    s.bad = s.first != lo || s.end != hi || s.nodes != s.end - s.first || s.len != raw;
     return s;
 }
 
@@ -291,6 +298,7 @@ __device__ __forceinline__ TreeUnits tree_units(const TreeParams &p, const TreeS
 struct TreeLine {
     int64_t total, before, mine;  // this thread's sequences [b0, b1) lie at [before, before + mine)
     int b0, b1, count, step, rest;
+    int floor;  // of sequence b0
 };
 
 template <int HEAD_DIM, int STREAMS, int THREADS>
@@ -301,21 +309,30 @@ __device__ __forceinline__ TreeLine tree_line(const TreeParams &p, int ctas, int
     TreeLine n;
     n.b0 = min((int)threadIdx.x * per, p.batch);
     n.b1 = min(n.b0 + per, p.batch);
-    n.mine = 0;
-    for (int b = n.b0; b < n.b1; ++b) {
-        const TreeSeq seq = tree_seq(p, b);
-        if (seq.bad && report) raise_flag(p.err_flag, PA_FLAG_BAD_LEN);
-        const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, seq);
-        n.mine += (int64_t)(u.chunks * p.kv_heads) * (u.tiles + C::kUnitCost);
-    }
-    int64_t incl = n.mine;
+    n.floor = 0;
+    int64_t incl;
+    for (bool ordered = true;;) {  // once, or a second time where bounds decrease
+        bool down = false;
+        n.mine = 0;
+        for (int b = n.b0, floor = n.floor; b < n.b1; ++b) {
+            const TreeSeq seq = tree_seq(p, b, floor);
+            if (seq.bad && report) raise_flag(p.err_flag, PA_FLAG_BAD_LEN);
+            const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, seq);
+            n.mine += (int64_t)(u.chunks * p.kv_heads) * (u.tiles + C::kUnitCost);
+            down |= tree_bound(p, b + 1) < tree_bound(p, b);
+            floor = seq.end;
+        }
+        incl = n.mine;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += up;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += up;
+        }
+        if (lane == 31) scan[warp] = incl;
+        if (!__syncthreads_or(ordered && down)) break;
+        ordered = false;
+        for (int b = 0; b < n.b0; ++b) n.floor = max(n.floor, tree_bound(p, b));
     }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
     n.before = incl - n.mine;
     n.total = 0;
 #pragma unroll
@@ -353,7 +370,7 @@ template <int HEAD_DIM, int STREAMS>
 __device__ __forceinline__ TreeMark tree_mark(const TreeParams &p, const TreeUnits &u, int b, int64_t at) {
     using C = TreeCfg<HEAD_DIM, STREAMS>;
     const int weight = u.tiles + C::kUnitCost;
-    TreeMark m{b, at <= INT32_MAX ? (int)at / weight : (int)(at / weight), 0};
+    TreeMark m{b, at <= INT32_MAX ? (int)at / weight : (int)(at / weight), 0, 0};
     const int tile = (int)(at - (int64_t)m.unit * weight) - C::kUnitCost;
     if (p.part_o ? tile > u.tiles - C::kSnap : 2 * tile >= u.tiles)
         ++m.unit;
@@ -371,14 +388,16 @@ __device__ __forceinline__ void tree_marks(const TreeParams &p, int ctas, int i,
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         int64_t at = tree_cut(n, i + k);
-        if (threadIdx.x == 0 && at >= n.total) mark[k] = TreeMark{p.batch, 0, 0};
+        if (threadIdx.x == 0 && at >= n.total) mark[k] = TreeMark{p.batch, 0, 0, 0};
         at -= n.before;
         if (at < 0 || at >= n.mine) continue;
-        for (int b = n.b0; b < n.b1; ++b) {
-            const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, tree_seq(p, b));
+        for (int b = n.b0, floor = n.floor; b < n.b1; ++b) {
+            const TreeSeq seq = tree_seq(p, b, floor);
+            const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, seq);
             const int64_t weight = (int64_t)(u.chunks * p.kv_heads) * (u.tiles + C::kUnitCost);
             if (at < weight) {
                 mark[k] = tree_mark<HEAD_DIM, STREAMS>(p, u, b, at);
+                mark[k].floor = floor;
                 if (k == 0) {
                     spot->line = n;
                     spot->begin = tree_cut(n, i) - at + (int64_t)mark[k].unit * (u.tiles + C::kUnitCost);
@@ -386,6 +405,7 @@ __device__ __forceinline__ void tree_marks(const TreeParams &p, int ctas, int i,
                 break;
             }
             at -= weight;
+            floor = seq.end;
         }
     }
     __syncthreads();
@@ -492,9 +512,9 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         TreeSeq seq{}, ahead{};
         TreeUnits of{};
         if (cur.b < p.batch) {
-            seq = tree_seq(p, cur.b);
+            seq = tree_seq(p, cur.b, cur.floor);
             of = tree_units<HEAD_DIM, STREAMS>(p, seq);
-            if (cur.b + 1 < p.batch) ahead = tree_seq(p, cur.b + 1);
+            if (cur.b + 1 < p.batch) ahead = tree_seq(p, cur.b + 1, seq.end);
         }
         // A tile to be loaded: this lane loads column box `box` of block `id` of it, if it has a page at all.
         struct Tile {
@@ -520,7 +540,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                     cur.unit = cur.tile = of.chunks = 0;
                     seq = ahead;
                     if (cur.b < p.batch) of = tree_units<HEAD_DIM, STREAMS>(p, seq);
-                    if (cur.b + 1 < p.batch) ahead = tree_seq(p, cur.b + 1);
+                    if (cur.b + 1 < p.batch) ahead = tree_seq(p, cur.b + 1, seq.end);
                 }
                 piece.h = of.chunks == 1 ? cur.unit : cur.unit / of.chunks;
                 piece.node0 = (cur.unit - piece.h * of.chunks) * (STREAMS * tile_nodes);
@@ -627,7 +647,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
             TreeJoin j{0, 0, 0, 0, 0, 0, {}};
             const TreeMark at = mark[0];
             if (at.b < p.batch && at.tile != 0) {
-                const TreeSeq q = tree_seq(p, at.b);
+                const TreeSeq q = tree_seq(p, at.b, at.floor);
                 const TreeUnits u = tree_units<HEAD_DIM, STREAMS>(p, q);
                 const TreeLine &line = spot->line;
                 auto inside = [&](int i) {  // cut i is one of this unit

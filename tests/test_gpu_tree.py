@@ -465,3 +465,34 @@ def test_python_refusals():
             pa.pa_decode_tree(out, *args, **kw)
     with pytest.raises(pa.PaError):
         pa.pa_decode_tree(out, *dev, **dict(kw, partition_tokens=100))
+
+
+@pytest.mark.parametrize("Hq,Hkv,extra", [(4, 2, 0), (8, 1, 2)])
+@pytest.mark.parametrize("pt", [-1, 128])
+def test_bounds_that_decrease(Hq, Hkv, extra, pt):
+    """Every row has one owner: a sequence that begins below an earlier bound has no nodes, the others keep theirs."""
+    import paged_kv_cache_349_b200 as pa
+    c = Case([900, 37, 1300, 700], [5, 3, 6, 6], Hq, Hkv, 64, 16, seed=4, masks="chain", extra_words=extra)
+    c.max_nodes = max(c.max_nodes, 9)
+    c.bits[:9] = np.arange(c.bits.shape[1]) <= np.arange(9)[:, None]
+    c.cu = np.array([0, 9, 5, 14, 20])  # rows 9..13 are nobody's
+    out = c.launch(pt)
+    assert c.flag == pa.PA_FLAG_BAD_LEN
+    assert bool((out[9:14] == 7.0).all())
+    c.counts, c.cu = [9, 0, 0, 6], np.array([0, 9, 9, 14, 20])
+    c.check(out, only=[0, 3])
+
+
+def test_a_bound_beyond_those_of_many_sequences():
+    """More sequences than threads: one bound that is too large takes the rows of all sequences below it."""
+    import paged_kv_cache_349_b200 as pa
+    B = 700
+    c = Case(np.random.default_rng(6).integers(0, 200, B), [1] * B, 4, 2, 64, 8, seed=6, masks="chain")
+    c.cu[3] = 600
+    for pt in (-1, 128):
+        out = c.launch(pt, max_len=600)
+        assert c.flag == pa.PA_FLAG_BAD_LEN
+        assert bool((out[3:600] == 7.0).all())
+        c.cu[3] = 3
+        c.check(out, only=[0, 1, 2, *range(600, B)])
+        c.cu[3] = 600
