@@ -792,7 +792,9 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 node = tile.node0 + s * tile_nodes + (r >> p.group_shift);
                 live = node < tile.nodes;
                 seen = dirty = false;
-                m = -INFINITY;
+                // Rows past the last node have the queries of whatever follows: no score of theirs may exceed their
+                // maximum and move the reference of the warp's other rows, which decides how their weights round.
+                m = live ? -INFINITY : INFINITY;
                 l = 0.f;
                 // the nodes of the first drafted tile that the row sees: needed at the end of the piece, fetched now
 #pragma unroll

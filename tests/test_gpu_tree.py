@@ -496,3 +496,28 @@ def test_a_bound_beyond_those_of_many_sequences():
         c.cu[3] = 3
         c.check(out, only=[0, 1, 2, *range(600, B)])
         c.cu[3] = 600
+
+
+@pytest.mark.parametrize("nodes,Hq,Hkv,d,extra", [(5, 8, 2, 128, 0), (9, 8, 2, 64, 0), (30, 8, 2, 128, 0), (3, 4, 4, 128, 0),
+                                                   (7, 16, 2, 128, 2), (17, 8, 1, 64, 0)])
+def test_uncut_results_do_not_depend_on_neighbours(nodes, Hq, Hkv, d, extra):
+    """The rows behind a tree's last node hold the next sequence's queries, or none: whatever their scores are, the
+    tree's own rows keep their bits.  Gain 30 makes the neighbour's maximum rise by dozens in tile after tile."""
+    import torch
+    neighbours = [700, 333]
+    c = Case([900, *neighbours], [nodes, 6, 16], Hq, Hkv, d, 16, seed=nodes, extra_words=extra, tail=2, poison=0.0)
+    quiet = c.launch(-1)
+    c.check(quiet)
+    for gain in (30.0, -200.0, float("nan"), float("inf")):
+        q = c.q.clone()
+        c.q[nodes:] *= gain
+        loud = c.launch(-1)
+        assert torch.equal(loud[:nodes], quiet[:nodes]), gain
+        c.q[:] = q
+    alone = Case([900], [nodes], Hq, Hkv, d, 16, seed=0)
+    alone.q, alone.kt, alone.vt, alone.k, alone.v = c.q[:nodes], c.kt[:nodes], c.vt[:nodes], c.k, c.v
+    alone.tables, alone.nb = c.tables[:1], c.nb
+    for most in (c.max_nodes, nodes):  # one or two groups of rows in a CTA
+        alone.max_nodes = most
+        alone.masks = np.ascontiguousarray(c.masks[:nodes, :-(-most // 32)])
+        assert torch.equal(alone.launch(-1), quiet[:nodes]), most
