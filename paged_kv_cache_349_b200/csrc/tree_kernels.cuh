@@ -45,6 +45,8 @@
 //    that see them.
 #pragma once
 
+#include <float.h>
+
 #include "pa_common.cuh"
 
 namespace pa {
@@ -748,8 +750,9 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         const int r = threadIdx.x & (kTileM - 1);
         const uint32_t base = tmem + s * C::kStreamCols + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t o_addr = base + C::kOCol;
-        const float c = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;  // a scale of 0 must not meet -inf
-        const float rise = kMaxRise / c;
+        // A scale of 0 must not meet -inf: the smallest value there is leaves every weight within 2^-20 of 1.
+        const float c = fmaxf(p.scale_log2, __int_as_float(1));
+        const float rise = fminf(kMaxRise / c, FLT_MAX);  // an infinite one would hide the first maximum (-inf + inf)
 
         // One thread of each stream loads its queries: the first piece's at once, the next one's when the
         // last scores of a piece are there, while their softmax and the piece's output are still to come.

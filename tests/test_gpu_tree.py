@@ -521,3 +521,17 @@ def test_uncut_results_do_not_depend_on_neighbours(nodes, Hq, Hkv, d, extra):
         alone.max_nodes = most
         alone.masks = np.ascontiguousarray(c.masks[:nodes, :-(-most // 32)])
         assert torch.equal(alone.launch(-1), quiet[:nodes]), most
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-45, 1e-40, 1e-38, 1.7e-38, 1e-30])
+@pytest.mark.parametrize("pt", [-1, 128])
+def test_scales_of_nothing(scale, pt):
+    """Down to the smallest fp32 and 0: all weights are the same, and what a row does not see stays out."""
+    for Hq, Hkv in ((4, 2), (8, 1)):
+        c = Case([0, 1, 300, 777], [5, 3, 40, 20], Hq, Hkv, 64, 16, seed=9)
+        c.scale = float(np.float32(scale))
+        c.check(c.launch(pt))
+    c = Case([0, 1, 300, 777], [5, 3, 40, 20], 4, 2, 64, 16, seed=9, gain=1e36)  # scores of up to 1e38
+    c.scale = float(np.float32(scale))
+    if scale < 1e-29:
+        c.check(c.launch(pt))
