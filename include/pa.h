@@ -596,7 +596,9 @@ int pa_tree_masks(int32_t *masks, int32_t *positions, const int32_t *parents, co
  *                  this many tokens or more (a multiple of 128; no cut when
  *                  max_seq_len is at most twice that), -1 = no cut: results
  *                  then do not depend on the rest of the batch.
- * scale          : finite and not negative (else PA_ERR_INVALID_ARG)
+ * scale          : not negative, and scale * log2(e) finite in fp32 (else
+ *                  PA_ERR_INVALID_ARG).  q.k has to stay within fp32; scale q.k
+ *                  need not.
  * workspace      : pa_decode_tree_workspace_size(...) bytes, 16-byte aligned
  *                  (may be NULL if that is 0); no initialisation needed.
  *                  Calls that may overlap on the GPU need one each.

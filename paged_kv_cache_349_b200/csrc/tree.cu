@@ -1,6 +1,8 @@
 // Host side of the attention of drafted tokens: tensor maps, the choice of
 // variant, the workspace and the launches (the device code is in
 // tree_kernels.cuh).
+#include <math.h>
+
 #include <mutex>
 
 #include "tree_kernels.cuh"
@@ -169,7 +171,7 @@ int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tre
         pa::bad_rows(v_tree, v_stride, num_kv_heads, head_dim))
         return PA_ERR_INVALID_ARG;
     if (partition_tokens > 0 && partition_tokens % 128) return PA_ERR_INVALID_ARG;
-    if (!(scale >= 0.f && scale < 3.0e38f)) return PA_ERR_INVALID_ARG;
+    if (!(scale >= 0.f && scale * pa::kTreeLog2e < HUGE_VALF)) return PA_ERR_INVALID_ARG;
     if (batch > 65535 || num_q_heads > 65535) return PA_ERR_UNSUPPORTED;
     const uint64_t rows = (uint64_t)num_blocks * (uint64_t)num_kv_heads * (uint64_t)block_size;
     if (rows >= (1ull << 31)) return PA_ERR_UNSUPPORTED;  // TMA row coordinate is int32

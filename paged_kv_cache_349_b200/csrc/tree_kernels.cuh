@@ -258,6 +258,20 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
     return w;
 }
 
+// m c is rounded, by up to 32 where it is below 2^30; further out that would make all weights of a row infinite or 0.
+// A score below the row's largest, m, is below it by m 2^-24 at least, as fp32 has it: out there it has no weight, and
+// the scale may as well be another.
+__device__ __forceinline__ bool tree_far(float m, float c) { return fabsf(m * c) > 0x1p30f && !isinf(m); }
+// The scale in log2 of such a row: the power of two that takes m exactly to between 2^31 and 2^32.
+__device__ __forceinline__ float tree_row_scale(float m, float c) {
+    return tree_far(m, c) ? __int_as_float(min(254 + 31 - ((__float_as_int(m) >> 23) & 255), 254) << 23) : c;
+}
+// The reference of a partial state in log2: that of such a row is beyond 2^30 too, and larger where m is.
+__device__ __forceinline__ float tree_reference(float m, float c) {
+    if (tree_far(m, c)) return copysignf((float)(__float_as_int(m) & 0x7fffffff) * 128.f, m);
+    return m == -INFINITY ? m : m * c;
+}
+
 // A bound between sequences' rows.
 __device__ __forceinline__ int tree_bound(const TreeParams &p, int i) { return min(max(__ldg(p.cu + i), 0), p.num_rows); }
 
@@ -776,7 +790,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
         uint32_t turns = 0;                    // so far
         uint2 cleanings = make_uint2(0u, 0u);  // so far, of one stream and of both
         uint32_t tree_bits[kWords] = {};  // the row's mask of the first drafted tile
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, row_c = c;
         bool ok = true;
         for (uint32_t t = 0;; ++t) {
             const uint32_t mt = t & (C::kMetas - 1);
@@ -799,6 +813,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 // maximum and move the reference of the warp's other rows, which decides how their weights round.
                 m = live ? -INFINITY : INFINITY;
                 l = 0.f;
+                row_c = c;
                 // the nodes of the first drafted tile that the row sees: needed at the end of the piece, fetched now
 #pragma unroll
                 for (int w = 0; w < kWords; ++w)
@@ -854,6 +869,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 const float down = next == -INFINITY ? 1.f : fast_exp2((m - next) * c);
                 m = next;
                 l *= down;
+                row_c = tree_row_scale(m, c);
                 if (!(flags & kFirst)) {  // O has been written: wait for the last product, then rescale it
                     ok = ring_wait<kBufs>(pv_done + kBufs * s, g - 1, p.err_flag);
                     if (!__all_sync(0xffffffffu, ok)) break;
@@ -886,8 +902,8 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 }
             }
             const uint32_t p_addr = base + C::kPCol + buf * (kTileN / 2);
-            const float bias = m == -INFINITY ? 0.f : -m * c;
-            const float2 c2 = make_float2(c, c), bias2 = make_float2(bias, bias);
+            const float bias = m == -INFINITY ? 0.f : -m * row_c;
+            const float2 c2 = make_float2(row_c, row_c), bias2 = make_float2(bias, bias);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int q = 0; q < kTileN / 32; ++q) {
@@ -1064,7 +1080,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
                 }
             }
             if (live && !whole)
-                *reinterpret_cast<float2 *>(p.part_ml + (state + r) * 2) = make_float2(m == -INFINITY ? m : m * c, l);
+                *reinterpret_cast<float2 *>(p.part_ml + (state + r) * 2) = make_float2(tree_reference(m, c), l);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free + s);

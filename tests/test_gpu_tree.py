@@ -535,3 +535,40 @@ def test_scales_of_nothing(scale, pt):
     c.scale = float(np.float32(scale))
     if scale < 1e-29:
         c.check(c.launch(pt))
+
+
+@pytest.mark.parametrize("scale", [1.0, 1e6, 1e8, 1e12, 1e30, 2.3e38])
+@pytest.mark.parametrize("pt", [-1, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (8, 1)])
+def test_scales_up_to_the_largest(scale, pt, Hq, Hkv):
+    """Scaled scores far beyond 2^30 and beyond fp32: a row is the mean of the values at its largest score.
+
+    Every key is 1, 2 or 3 in all dimensions and q is 1, -1, 0 or 2^-7, so that scores are exact and other scores are at
+    least 2^-1 scale below, or (q = 0) the same.  The mean's weights are all alike: 2^-8 of it for their rounding, which
+    their sum does not have, 2^-8 for the output's, 2^-13 for fp32 sums of 1000 terms.  Where scale is 1 the others have
+    weights: the definition's own tolerance.
+    """
+    import torch
+    c = Case([700, 0, 300, 65], [12, 3, 40, 1], Hq, Hkv, 64, 16, seed=3, masks="chain", poison=0.0)
+    c.scale = float(np.float32(scale))
+    rng = np.random.default_rng(1)
+    for keys in (c.k, c.kt):
+        a = torch.from_numpy(rng.integers(1, 4, keys.shape[:-1])).to(torch.bfloat16)
+        keys[:] = a[..., None]
+    for h in range(Hq):
+        c.q[:, h] = (1.0, -1.0, 0.0, 2.0 ** -7)[h % 4]
+    out = c.launch(pt, fill=255)
+    assert c.flag == 0
+    if scale == 1.0:
+        return c.check(out)
+    got = out.double().cpu().numpy()
+    for b in range(4):
+        k, v = (x[:, 0] for x in c.rows(b))
+        for i in range(c.counts[b]):
+            seen = np.concatenate([np.ones(c.lens[b], bool), c.bits[c.cu[b] + i, :c.counts[b]]])
+            for h in range(Hq):
+                score = k[seen] @ c.q[c.cu[b] + i, h].double().numpy()
+                best = v[seen][score == score.max()]
+                want, A = best.mean(0), np.abs(best).mean(0)
+                err = np.abs(got[c.cu[b] + i, h] - want)
+                assert (err <= np.abs(want) * 2.0 ** -8 + A * (2.0 ** -8 + 2.0 ** -13)).all(), (b, i, h)

@@ -163,3 +163,16 @@ def test_tree_workspace_size_of_unsplit_calls():
     assert pa.pa_decode_tree_workspace_size(4, 32, 8, 2, 128, 16, 512, 8, 0) == 0  # a few tiles: never cut
     assert pa.pa_decode_tree_workspace_size(4, 32, 8, 2, 128, 16, 256, 8, 128) == 0
     assert pa.pa_decode_tree_workspace_size(4, 32, 8, 2, 128, 16, 4096, 8, 0) > 0
+
+
+def test_decode_tree_scales():
+    """A scale is accepted up to where scale * log2(e) leaves fp32.  The scale is looked at before the batch, which is
+    too large here, so that no call goes on."""
+    def call(scale):
+        return lib.pa_decode_tree(ptr(), ptr(), 1024, ptr(), 256, ptr(), 256, 8, ptr(), ptr(), ptr(), 4, ptr(), ptr(), ptr(),
+                                  70000, 64, 4, 8, 2, 128, 16, 64, scale, -1, None, 0, None, None)
+
+    for good in (0.0, 1e-45, 1.0, 2.3e38):
+        assert call(good) == UNSUPPORTED, good
+    for bad in (2.4e38, 2.9e38, math.inf, math.nan, -1e-45):
+        assert call(bad) == INVALID, bad
