@@ -648,8 +648,13 @@ int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tre
  *                 starting at cu_rows[b] (device int32 [batch + 1]), and its
  *                 k-th new token is node path[b, k] (device int32
  *                 [batch, max_path]; a node named twice counts where it is
- *                 named first).  All other rows get slot -1.  add_lens[b] >
- *                 max_path sets PA_FLAG_BAD_LEN, the sequence gets no token.
+ *                 named first).  All other rows get slot -1.  A path that
+ *                 ends before add_lens[b] names (at max_path or a negative
+ *                 entry) sets PA_FLAG_BAD_LEN, the sequence gets no token.
+ *                 Names are not compared with each other or with the tree: a
+ *                 token named by a repeat, or by no node, still counts for the
+ *                 length, no row gets its slot, and its place in the cache keeps
+ *                 what it held.  The caller names add_lens[b] different nodes.
  * All or nothing: when the free list does not hold the blocks
  * (PA_FLAG_NO_BLOCKS), or num_rows does not hold the packed tokens
  * (PA_FLAG_BAD_LEN), lengths, tables and cursor stay as they were, every slot

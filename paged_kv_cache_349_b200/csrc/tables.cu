@@ -139,7 +139,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan_kernel(const Exte
         if (b >= p.batch) return;
         len = p.lens[b];  // may be lens_out: read before any write of this sequence
         add = __ldg(p.add + b);
-        if (len < 0 || add < 0 || (int64_t)len + add > cap || (p.path && add > p.max_path)) {
+        bool ok = len >= 0 && add >= 0 && (int64_t)len + add <= cap;
+        if (p.path && ok) {  // as many tokens as the path has names: one without a row would leave a hole in the cache
+            ok = add <= p.max_path;
+            for (int k = 0; ok && k < add; ++k) ok = __ldg(p.path + (int64_t)b * p.max_path + k) >= 0;
+        }
+        if (!ok) {
             if (report) raise_flag(p.err_flag, PA_FLAG_BAD_LEN);
             add = 0;
         }

@@ -289,3 +289,20 @@ def test_tree_masks_of_more_sequences_than_threads():
     want[3:600] = wpos[3:600] = 0  # row 2 is the first node of the sequence that ends at 600
     assert int(flag.item()) == pa.PA_FLAG_BAD_LEN
     assert np.array_equal(host(masks)[:, 0], want) and np.array_equal(host(pos), wpos)
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31])
+def test_paths_that_end_early(bad):
+    """A negative entry among the accepted ones: that sequence gets no token and is flagged, the others get theirs."""
+    import paged_kv_cache_349_b200 as pa
+    rng = np.random.default_rng(1)
+    bs, lens, add = 8, np.array([7, 3, 0, 30]), np.array([3, 2, 4, 1])
+    cu = np.array([0, 6, 9, 14, 20])
+    whole = np.array([[0, 2, 5, -1], [0, 1, -1, -1], [0, 1, 3, 4], [2, -1, -1, -1]])
+    tables, free, nb = batch(rng, lens, bs, add, 2)
+    for b, k in ((0, 0), (0, 2), (1, 1), (2, 3), (3, 0)):
+        path, kept = whole.copy(), add.copy()
+        path[b, k], kept[b] = bad, 0
+        want = model(tables, lens, kept, free, 0, bs, 20, cu, whole)
+        same(run(tables, lens, add, free, 0, bs, 20, nb, cu, path), (*want[:-1], pa.PA_FLAG_BAD_LEN))
+    same(run(tables, lens, add, free, 0, bs, 20, nb, cu, whole), model(tables, lens, add, free, 0, bs, 20, cu, whole))
