@@ -656,9 +656,9 @@ int pa_decode_tree(void *out, const void *q, int64_t q_stride, const void *k_tre
  *                 length, no row gets its slot, and its place in the cache keeps
  *                 what it held.  The caller names add_lens[b] different nodes.
  * All or nothing: when the free list does not hold the blocks
- * (PA_FLAG_NO_BLOCKS), or num_rows does not hold the packed tokens
- * (PA_FLAG_BAD_LEN), lengths, tables and cursor stay as they were, every slot
- * is -1 and cu_tokens is all zero.
+ * (PA_FLAG_NO_BLOCKS), num_rows does not hold the packed tokens, or cu_rows
+ * decreases or leaves [0, num_rows] (PA_FLAG_BAD_LEN), lengths, tables and
+ * cursor stay as they were, every slot is -1 and cu_tokens is all zero.
  * No two pointers overlap except where it says so.  batch == 0 launches
  * nothing. */
 int pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,

@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan_kernel(const Exte
     const int cursor = *p.cursor;  // may be cursor_out
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
     int len = 0, add = 0, blocks = 0;
+    int unordered = 0;  // bounds of drafted rows that decrease or leave the rows: a token could miss its row
     int64_t tok_before = 0, blk_before = 0, tok_total, blk_total;
     auto read = [&](int b, bool report) {
         len = add = blocks = 0;
@@ -140,6 +141,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan_kernel(const Exte
         len = p.lens[b];  // may be lens_out: read before any write of this sequence
         add = __ldg(p.add + b);
         bool ok = len >= 0 && add >= 0 && (int64_t)len + add <= cap;
+        if (p.path && report) {
+            const int lo = __ldg(p.cu_rows + b), hi = __ldg(p.cu_rows + b + 1);
+            unordered |= lo < 0 || hi < lo || hi > p.num_rows;
+        }
         if (p.path && ok) {  // as many tokens as the path has names: one without a row would leave a hole in the cache
             ok = add <= p.max_path;
             for (int k = 0; ok && k < add; ++k) ok = __ldg(p.path + (int64_t)b * p.max_path + k) >= 0;
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan_kernel(const Exte
         all_tok += tok_total;
         all_blk += blk_total;
     }
-    int bad = 0;
+    int bad = p.path && __syncthreads_or(unordered) ? PA_FLAG_BAD_LEN : 0;
     if (cursor < 0 || cursor + all_blk > p.num_free) bad |= PA_FLAG_NO_BLOCKS;
     if (all_tok > (p.path ? (int64_t)INT32_MAX : (int64_t)p.num_rows)) bad |= PA_FLAG_BAD_LEN;
     if (bad && threadIdx.x == 0) raise_flag(p.err_flag, bad);

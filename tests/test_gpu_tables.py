@@ -306,3 +306,16 @@ def test_paths_that_end_early(bad):
         want = model(tables, lens, kept, free, 0, bs, 20, cu, whole)
         same(run(tables, lens, add, free, 0, bs, 20, nb, cu, path), (*want[:-1], pa.PA_FLAG_BAD_LEN))
     same(run(tables, lens, add, free, 0, bs, 20, nb, cu, whole), model(tables, lens, add, free, 0, bs, 20, cu, whole))
+
+
+@pytest.mark.parametrize("cu", [[0, 9, 6, 14], [-1, 6, 9, 14], [0, 6, 9, 21], [3, 1, 9, 14], [0, 6, 9, 2 ** 31 - 1]])
+def test_bounds_of_drafted_rows(cu):
+    """Bounds that decrease or leave the rows: nothing changes, no row gets a slot."""
+    import paged_kv_cache_349_b200 as pa
+    rng = np.random.default_rng(2)
+    lens, add = np.array([7, 3, 0]), np.array([3, 2, 4])
+    path = np.array([[0, 2, 5, -1], [0, 1, -1, -1], [0, 1, 3, 4]])
+    tables, free, nb = batch(rng, lens, 8, add, 2)
+    for in_place in (True, False):
+        got = run(tables, lens, add, free, 0, 8, 20, nb, np.array(cu), path, in_place=in_place)
+        same(got, (tables, lens, 0, np.full(20, -1), np.zeros(20), np.zeros(4), pa.PA_FLAG_BAD_LEN))
