@@ -684,7 +684,8 @@ int pa_extend_tables(int32_t *block_tables, int max_blocks_per_seq, const int32_
  *             of one projection's output.  Strides are multiples of 8 and no
  *             smaller than a row; buffers are 16-byte aligned.
  * q_out, k_out : rows as q and k, with strides of their own; may be q and k
- *             themselves (same stride), else no overlap with any input
+ *             themselves (same stride, else PA_ERR_INVALID_ARG); no other
+ *             overlap with any input
  * positions : device int32 [num_tokens]
  * turns     : device double [rotary_dim / 2], from pa_rope_frequencies
  * rotary_dim: a multiple of 16, 16 .. head_dim (else PA_ERR_UNSUPPORTED)

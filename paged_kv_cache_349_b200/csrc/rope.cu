@@ -213,6 +213,10 @@ int rope_impl(RopeParams p, int head_dim, int interleaved, bool cache, bool fp8,
                       bad_rows(p.q_out, p.q_out_stride, p.q_heads, head_dim)))
         return PA_ERR_INVALID_ARG;
     if (p.kv_heads && bad_rows(p.k, p.k_stride, p.kv_heads, head_dim)) return PA_ERR_INVALID_ARG;
+    // in place at another stride, rows would be written that others have still to read
+    if (p.num_tokens > 1 && ((p.q_heads && p.q == p.q_out && p.q_stride != p.q_out_stride) ||
+                             (p.kv_heads && p.k == p.k_out && p.k_stride != p.k_out_stride)))
+        return PA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (head_dim == 128)
         interleaved ? launch_rope<128, true>(p, cache, fp8, s) : launch_rope<128, false>(p, cache, fp8, s);

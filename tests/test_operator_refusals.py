@@ -176,3 +176,17 @@ def test_decode_tree_scales():
         assert call(good) == UNSUPPORTED, good
     for bad in (2.4e38, 2.9e38, math.inf, math.nan, -1e-45):
         assert call(bad) == INVALID, bad
+
+
+def test_rope_in_place_needs_one_stride():
+    """A row written in place at another stride would land on rows that are still to be read."""
+    names = ROPE + "ko kos Hkv pos turns rot inter gain T d stream".split()
+    call = caller(lib.pa_rope, names, q=ptr(), qs=1024, qo=ptr(0x20000), qos=1024, Hq=8, k=ptr(0x30000), ks=256, ko=ptr(0x40000),
+                  kos=256, Hkv=2, pos=ptr(), turns=ptr(), rot=128, inter=0, gain=1.0, T=3, d=128, stream=None)
+    assert call(qo=ptr(), qos=1032) == INVALID and call(qo=ptr(), qs=2048) == INVALID
+    assert call(ko=ptr(0x30000), kos=264) == INVALID and call(ko=ptr(0x30000), ks=512) == INVALID
+    names = ROPE + "v vs Hkv kc vc slots NB bs pos turns rot inter gain T d flag stream".split()
+    call = caller(lib.pa_rope_and_cache, names, q=ptr(), qs=1024, qo=ptr(), qos=1032, Hq=8, k=ptr(0x30000), ks=256,
+                  v=ptr(0x40000), vs=256, Hkv=2, kc=ptr(0x50000), vc=ptr(0x60000), slots=ptr(), NB=8, bs=16, pos=ptr(),
+                  turns=ptr(), rot=64, inter=1, gain=1.0, T=3, d=128, flag=None, stream=None)
+    assert call() == INVALID
