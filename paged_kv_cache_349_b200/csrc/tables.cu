@@ -147,7 +147,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) extend_plan_kernel(const Exte
         }
         if (p.path && ok) {  // as many tokens as the path has names: one without a row would leave a hole in the cache
             ok = add <= p.max_path;
-            for (int k = 0; ok && k < add; ++k) ok = __ldg(p.path + (int64_t)b * p.max_path + k) >= 0;
+            int least = 0;  // no early end: the loads do not wait for each other
+#pragma unroll 8
+            for (int k = 0; k < (ok ? add : 0); ++k) least = min(least, __ldg(p.path + (int64_t)b * p.max_path + k));
+            ok &= least >= 0;
         }
         if (!ok) {
             if (report) raise_flag(p.err_flag, PA_FLAG_BAD_LEN);
