@@ -216,69 +216,82 @@ __global__ void __launch_bounds__(kMapThreads) extend_map_kernel(const ExtendPar
 // ---------------------------------------------------------------------------
 
 constexpr int kMaskThreads = 256;
+// CTAs for each SM (two rounds of eight) before one takes several sequences: the bounds before a CTA's sequences are
+// read by all of them.  Measured (calls back to back) with one sequence to a CTA | 8 | 16 CTAs: 1200 trees of 100
+// 6.5 | 8.1 | 6.5 us, 4096 of 8 10.1 | 8.4 | 9.1, 65536 of 2 462 | 85 | 88.
+constexpr int kMaskCtasPerSm = 16;
 
 // 6.2 us for 256 trees of up to 256 nodes (0.3 us of bytes; an empty launch of this size takes 4).
-// One CTA for each sequence: every thread walks the ancestors of its nodes, which
-// takes as many steps as the tree is deep, and sets their bits in a mask row of
-// its own.  CTA `batch` clears the rows that belong to no sequence.
+// A CTA for each sequence, or for several in turn where there are many: every thread walks the
+// ancestors of its nodes, which takes as many steps as the tree is deep, and sets their bits in a mask row of its own.
+// Item `batch` clears the rows that belong to no sequence.
 __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(
     int32_t *__restrict__ masks, int32_t *__restrict__ positions, const int32_t *__restrict__ parents,
     const int32_t *__restrict__ cu, const int32_t *__restrict__ lens, int batch, int num_rows, int max_nodes,
-    int words, int32_t *__restrict__ err_flag) {
+    int words, int per_cta, int32_t *__restrict__ err_flag) {
     extern __shared__ int32_t s_tree[];
     int32_t *s_parent = s_tree;             // [max_nodes]
     int32_t *s_mask = s_tree + max_nodes;   // [max_nodes, words]
     __shared__ int s_floor;
-    const int b = blockIdx.x;
     auto bound = [&](int i) { return min(max(__ldg(cu + i), 0), num_rows); };
     auto clear = [&](int lo, int hi) {
         for (int64_t x = (int64_t)lo * words + threadIdx.x; x < (int64_t)hi * words; x += kMaskThreads) masks[x] = 0;
         if (positions)
             for (int r = lo + threadIdx.x; r < hi; r += kMaskThreads) positions[r] = 0;
     };
-    // Each row is written by one CTA, whatever the bounds: the rows of CTA b begin at the largest of bounds 0 .. b.
-    // A sequence that begins below an earlier bound would lose its first nodes there and is left without any.
-    const int lo = bound(b);
-    int top = 0;
-    for (int j = threadIdx.x; j < b; j += kMaskThreads) top = max(top, bound(j));
-    if (threadIdx.x == 0) s_floor = 0;
-    int start = lo;
-    if (__syncthreads_or(top > lo)) {
-        atomicMax(&s_floor, top);
+    const unsigned b0 = blockIdx.x * per_cta, b1 = min(b0 + per_cta, batch + 1u);
+    int top = 0;  // of the earlier bounds, over all threads
+    for (unsigned j = threadIdx.x; j < b0; j += kMaskThreads) top = max(top, bound(j));
+    for (unsigned x = b0; x < b1; ++x) {
+        const int b = (int)x;
+        // Each row is written by one CTA, whatever the bounds: the rows of sequence b begin at the largest of bounds
+        // 0 .. b.  A sequence that begins below an earlier bound would lose its first nodes there and is left without
+        // any.  Its nodes' parents are read before that is known.
+        const int lo = bound(b), hi = b < batch ? bound(b + 1) : lo;
+        int n = min(max(hi - lo, 0), max_nodes);
+        bool late = false;
+        for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+            int parent = __ldg(parents + lo + i);
+            if (parent < -1 || parent >= i) {
+                late = true;
+                parent = -1;
+            }
+            s_parent[i] = parent;
+        }
+        int start = lo;
+        if (__syncthreads_or(top > lo)) {
+            if (threadIdx.x == 0) s_floor = 0;
+            __syncthreads();
+            atomicMax(&s_floor, top);
+            __syncthreads();
+            start = s_floor;
+            n = 0;
+            late = false;
+        }
+        top = max(top, lo);
+        if (b == batch) {
+            clear(0, bound(0));
+            clear(start, num_rows);
+            return;
+        }
+        const int end = max(hi, start);
+        if (threadIdx.x == 0 && (start != __ldg(cu + b) || end != __ldg(cu + b + 1) || n != end - start))
+            raise_flag(err_flag, PA_FLAG_BAD_LEN);
+        if (late) raise_flag(err_flag, PA_FLAG_BAD_TREE);
+        for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+            int32_t *row = s_mask + i * words;
+            for (int w = 0; w < words; ++w) row[w] = 0;
+            int depth = -1;
+            for (int j = i; j >= 0; j = s_parent[j]) {  // parents come first: the walk ends
+                row[j >> 5] |= 1u << (j & 31);
+                ++depth;
+            }
+            if (positions) positions[lo + i] = __ldg(lens + b) + depth;
+        }
         __syncthreads();
-        start = s_floor;
+        for (int x = threadIdx.x; x < n * words; x += kMaskThreads) masks[(int64_t)lo * words + x] = s_mask[x];
+        clear(start + n, end);
     }
-    if (b == batch) {
-        clear(0, bound(0));
-        clear(start, num_rows);
-        return;
-    }
-    const int end = max(bound(b + 1), start);
-    const int n = start == lo ? min(end - start, max_nodes) : 0;
-    if (threadIdx.x == 0 && (start != __ldg(cu + b) || end != __ldg(cu + b + 1) || n != end - start))
-        raise_flag(err_flag, PA_FLAG_BAD_LEN);
-    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
-        int parent = __ldg(parents + lo + i);
-        if (parent < -1 || parent >= i) {
-            raise_flag(err_flag, PA_FLAG_BAD_TREE);
-            parent = -1;
-        }
-        s_parent[i] = parent;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
-        int32_t *row = s_mask + i * words;
-        for (int w = 0; w < words; ++w) row[w] = 0;
-        int depth = -1;
-        for (int j = i; j >= 0; j = s_parent[j]) {  // parents come first: the walk ends
-            row[j >> 5] |= 1u << (j & 31);
-            ++depth;
-        }
-        if (positions) positions[lo + i] = __ldg(lens + b) + depth;
-    }
-    __syncthreads();
-    for (int x = threadIdx.x; x < n * words; x += kMaskThreads) masks[(int64_t)lo * words + x] = s_mask[x];
-    clear(start + n, end);
 }
 
 }  // namespace
@@ -355,8 +368,9 @@ int pa_tree_masks(int32_t *masks, int32_t *positions, const int32_t *parents, co
     const int words = (max_nodes + 31) / 32;
     const size_t smem = (size_t)max_nodes * (words + 1) * 4;
     static_assert(PA_TREE_MAX_NODES * (PA_TREE_MAX_NODES / 32 + 1) * 4 <= 48 * 1024, "fits without an opt-in");
-    pa::tree_masks_kernel<<<(unsigned)batch + 1, pa::kMaskThreads, smem, static_cast<cudaStream_t>(stream)>>>(
-        masks, positions, parents, cu_nodes, seq_lens, batch, num_rows, max_nodes, words, err_flag);
+    const int per_cta = batch / (pa::kMaskCtasPerSm * pa::device_sm_count()) + 1;
+    pa::tree_masks_kernel<<<(unsigned)(batch / per_cta) + 1, pa::kMaskThreads, smem, static_cast<cudaStream_t>(stream)>>>(
+        masks, positions, parents, cu_nodes, seq_lens, batch, num_rows, max_nodes, words, per_cta, err_flag);
     pa::count_launch();
     return pa::launch_status();
 }

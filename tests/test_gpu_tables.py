@@ -319,3 +319,23 @@ def test_bounds_of_drafted_rows(cu):
     for in_place in (True, False):
         got = run(tables, lens, add, free, 0, 8, 20, nb, np.array(cu), path, in_place=in_place)
         same(got, (tables, lens, 0, np.full(20, -1), np.zeros(20), np.zeros(4), pa.PA_FLAG_BAD_LEN))
+
+
+@pytest.mark.parametrize("B,n", [(2367, 2), (2368, 2), (5000, 3), (20000, 1)])
+def test_tree_masks_of_many_sequences(B, n):
+    """More sequences than CTAs, in order and with a bound that is too large among the sequences of one CTA."""
+    import torch
+    import paged_kv_cache_349_b200 as pa
+    cu, lens, rows = np.arange(B + 1) * n, np.arange(B), B * n + 1
+    parents = np.append(np.tile(np.arange(n) - 1, B), 7)  # chains; the last row is nobody's
+    masks, pos, flag = torch.full((rows, 1), -1, dtype=torch.int32, device="cuda"), i32_dev(np.full(rows, 9)), i32_dev([0])
+    want, wpos = masks_model(parents, cu, lens, rows, n)
+    pa.pa_tree_masks(masks, pos, i32_dev(parents), i32_dev(cu), i32_dev(lens), max_nodes=n, err_flag=flag)
+    assert np.array_equal(host(masks), want) and np.array_equal(host(pos), wpos) and int(flag.item()) == 0
+    at, to = B // 3, B // 3 + 50
+    cu[at] = to * n  # sequence at - 1 reaches up to sequence `to`, with n nodes at most; those between have none
+    want[at * n:to * n] = wpos[at * n:to * n] = 0
+    masks.fill_(-1)
+    pa.pa_tree_masks(masks, pos, i32_dev(parents), i32_dev(cu), i32_dev(lens), max_nodes=n, err_flag=flag)
+    assert np.array_equal(host(masks), want) and np.array_equal(host(pos), wpos)
+    assert int(flag.item()) == pa.PA_FLAG_BAD_LEN
