@@ -604,7 +604,10 @@ int pa_tree_masks(int32_t *masks, int32_t *positions, const int32_t *parents, co
  *                  Calls that may overlap on the GPU need one each.
  * A block id outside [0, num_blocks) sets PA_FLAG_BAD_BLOCK and its tokens
  * are left out.  Other arguments, layouts and errors: as pa_decode.
- * Products take bf16 operands and accumulate in fp32; the softmax is fp32. */
+ * Products take bf16 operands and accumulate in fp32; the softmax is fp32.
+ * Each weight is rounded to one bf16 for its product with v (2^-8 of it at
+ * most) and the output to bf16; pa_decode keeps two bf16 parts and returns
+ * fp32, so that the two differ for the same row as bf16 values do. */
 size_t pa_decode_tree_workspace_size(int batch, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
                                      int block_size, int max_seq_len, int max_nodes, int partition_tokens);
 

@@ -24,7 +24,8 @@
 //  * Four warps for each 128 rows run the softmax, a row to a thread: no shuffles.
 //    P goes back to TMEM as bf16: 8 significant bits for each weight, as many as the
 //    values it multiplies have, and as the output keeps; the sum of the weights is
-//    fp32 and unrounded.
+//    fp32 and unrounded.  (pa_decode keeps two parts of a weight and returns fp32;
+//    a second part here would need 64 more columns than TMEM has for a CTA.)
 //  * A tile is 64 tokens: a thread holds its row's 64 scores in registers, which frees
 //    the score buffer for the next tile's product while the exponentials run, and P
 //    has two buffers, so that neither product is waited for.  128-token tiles in one
@@ -266,7 +267,8 @@ __device__ __forceinline__ bool tree_far(float m, float c) { return fabsf(m * c)
 __device__ __forceinline__ float tree_row_scale(float m, float c) {
     return tree_far(m, c) ? __int_as_float(min(254 + 31 - ((__float_as_int(m) >> 23) & 255), 254) << 23) : c;
 }
-// The reference of a partial state in log2: that of such a row is beyond 2^30 too, and larger where m is.
+// The reference of a partial state in log2: that of such a row is beyond 2^30 too, and larger where m is by 2^-17 of it
+// or more.  (A sum of 64 or 128 products in fp32 is not known any better.)
 __device__ __forceinline__ float tree_reference(float m, float c) {
     if (tree_far(m, c)) return copysignf((float)(__float_as_int(m) & 0x7fffffff) * 128.f, m);
     return m == -INFINITY ? m : m * c;
@@ -505,6 +507,7 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
     tree_marks<HEAD_DIM, STREAMS, C::kThreads>(p, gridDim.x, blockIdx.x, scan, mark, spot, blockIdx.x == 0);  // synchronises
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    // The joining CTAs find room only where CTAs of this grid have ended: this hides their launch, not their wait.
     if (p.part_o) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The tiles of this CTA are numbered through all its pieces: tile t has slot t of K's ring and of V's.
@@ -1108,8 +1111,9 @@ __global__ void __launch_bounds__(TreeCfg<HEAD_DIM, STREAMS>::kThreads, TreeCfg<
 constexpr int kJoinWarps = 8;
 constexpr int kJoinRows = 32;
 // Pieces that a warp joins alone: where all CTAs of the grid are on the GPU at once, and where they are not and the
-// CTAs of the other cuts would only be in the way.  Measured with 4 | 8 for both: 8 sequences of 32768 tokens with 128
-// rows of each kv head (two waves) 196 | 193 us; 2 of up to 13545 with 40/40 heads and 16 rows 62 | 65 us.
+// CTAs of the other cuts would only be in the way.  Measured with 2 | 3 | 4 | 8 for the first: 2 sequences of up to
+// 13545 tokens with 40/40 heads and 16 rows of each kv head 94.8 | 94.8 | 95.2 | 96.0 us, 16 of up to 4096 with 32/8
+// heads 51.8 | 51.7 | 52.2 | 52.0; with 3 | 8 for the second: 4 of up to 8190 with 64/8 heads and 512 rows 88.5 | 87.0.
 constexpr int kJoinAlone = 3, kJoinAloneWaves = 8;
 
 template <int HEAD_DIM, int STREAMS>
